@@ -394,9 +394,10 @@ def _plain_resize(s, seqs, lens):
     s["table"][seqs] = rows
     last = rows.gather(1, (had - 1).clamp(min=0)[:, None])[:, 0].clamp(min=0).long()
     shared = (lens > old) & (old % ps != 0) & (s["refs"][last] > 1)
-    s["refs"].index_add_(0, last[shared], -torch.ones_like(last[shared], dtype=torch.int32))
     first = had - shared.long()
     fits = _give(s, seqs, first, (gets - first).clamp(min=0), shared, last, gets)
+    left = last[shared & fits]
+    s["refs"].index_add_(0, left, -torch.ones_like(left, dtype=torch.int32))
     s["kv_len"][seqs] = torch.where(fits, lens, old).to(torch.int32)
 
 
