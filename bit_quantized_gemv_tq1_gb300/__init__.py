@@ -10,6 +10,9 @@ _EXPORTS = (
     "tq1_get_rows", "tq1_sync_status", "tq1_blocks_bytes", "tq1_q8_1_bytes", "tq2_quantize_rows", "tq2_mmv",
     "tq2_mmv_partials", "tq2_blocks_bytes", "tq2_dequantize_rows", "tq2_get_rows", "tq2_mmv_id",
     "tq2_mmv_id_slots", "tq2_mmv_f32", "tq2_mmv_add", "Tq1Error", "library", "library_path", "STATUS",
+    "tq1_kv_cache", "tq1_kv_batch", "tq1_rope_freqs", "tq1_rope_append", "tq1_paged_attn",
+    "tq1_paged_attn_workspace_size", "tq1_page_pool", "tq1_pages_copy", "tq1_pages_resize", "tq1_pages_fork",
+    "tq1_pages_compact", "tq1_pages_workspace_size",
 )
 __all__ = list(_EXPORTS)
 

@@ -20,9 +20,32 @@ TQ1_OK = 0
 STATUS = {
     0: "TQ1_OK", -1: "TQ1_ERR_NULL", -2: "TQ1_ERR_SHAPE", -3: "TQ1_ERR_ALIGN", -4: "TQ1_ERR_UNSUPPORTED",
     -5: "TQ1_ERR_WORKSPACE", -6: "TQ1_ERR_CUDA", -7: "TQ1_ERR_TIMEOUT", -8: "TQ1_ERR_BAD_ID",
+    -9: "TQ1_ERR_NO_PAGES",
 }
 BLOCK_BYTES = 54
 Q8_BYTES = 36
+TQ1_F32, TQ1_F16, TQ1_BF16 = 0, 1, 2
+
+
+class KvCache(ctypes.Structure):
+    """tq1_kv_cache; made by tq1_kv_cache(), which keeps the tensors alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_kv", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class KvBatch(ctypes.Structure):
+    """tq1_kv_batch; made by tq1_kv_batch()."""
+    _fields_ = [("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
+
+
+class PagePool(ctypes.Structure):
+    """tq1_page_pool; made by tq1_page_pool()."""
+    _fields_ = [("base", ctypes.c_void_p), ("n_pools", ctypes.c_int64), ("pool_stride", ctypes.c_int64),
+                ("page_bytes", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("refs", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("n_seqs", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("page_size", ctypes.c_int64)]
 
 
 class Tq1Error(RuntimeError):
@@ -92,12 +115,26 @@ def library() -> ctypes.CDLL:
         lib.tq1_dequantize_rows.argtypes = [P, P, I64, I64, ctypes.c_int, P]
         lib.tq1_get_rows.argtypes = [P, P, I64, P, I64, I64, ctypes.c_int, P]
         lib.tq1_sync_status.argtypes = [P]
+        C, B, G, INT, F32, F64 = (ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch), ctypes.POINTER(PagePool),
+                                  ctypes.c_int, ctypes.c_float, ctypes.c_double)
+        lib.tq1_rope_freqs.argtypes = [P, I64, F64, F64, F64, F64, F64, P]
+        lib.tq1_rope_append.argtypes = [C, B, P, I64, P, I64, P, I64, INT, P, I64, I64, P, I64, INT, F32, P, P]
+        lib.tq1_paged_attn_workspace_size.restype = SZ
+        lib.tq1_paged_attn_workspace_size.argtypes = [C, I64, I64, I64]
+        lib.tq1_paged_attn.argtypes = [C, B, P, I64, I64, I64, F32, INT, I64, P, I64, INT, P, SZ, P]
+        lib.tq1_pages_workspace_size.restype = SZ
+        lib.tq1_pages_workspace_size.argtypes = [G]
+        lib.tq1_pages_copy.argtypes = [G, P, P, I64, P]
+        lib.tq1_pages_resize.argtypes = [G, P, P, I64, P, SZ, P]
+        lib.tq1_pages_fork.argtypes = [G, P, P, I64, P, SZ, P]
+        lib.tq1_pages_compact.argtypes = [G, P, SZ, P]
         for name in ("tq1_quantize_rows", "q8_1_quantize_acts", "tq1_mmv", "tq1_mmv_add", "tq1_mmv_f32",
                      "tq1_mmv_partials", "tq1_mmv_id", "tq1_mmv_id_slots", "tq1_mmv_id_noalloc",
                      "tq1_dequantize_rows", "tq1_get_rows", "tq1_sync_status", "tq2_quantize_rows",
                      "tq2_mmv", "tq2_mmv_partials", "tq2_dequantize_rows", "tq2_get_rows", "tq2_mmv_id",
                      "tq2_mmv_id_slots", "tq2_mmv_f32", "tq2_mmv_add", "tq1_mmv_id_partials",
-                     "tq2_mmv_id_partials", "tq1_mmv_ws", "tq2_mmv_ws"):
+                     "tq2_mmv_id_partials", "tq1_mmv_ws", "tq2_mmv_ws", "tq1_rope_freqs", "tq1_rope_append",
+                     "tq1_paged_attn", "tq1_pages_copy", "tq1_pages_resize", "tq1_pages_fork", "tq1_pages_compact"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -298,3 +335,141 @@ def tq2_get_rows(blocks, row_ids, n_ids: int, out, n: int, k: int, out_f16: bool
 def tq1_sync_status(stream=None) -> int:
     """Synchronise the stream; return (and clear) the device status code."""
     return int(library().tq1_sync_status(_stream(stream)))
+
+
+# ------------------------------------------------ paged key/value cache --
+def _dtype(x) -> int:
+    import torch
+    try:
+        return {torch.float32: TQ1_F32, torch.float16: TQ1_F16, torch.bfloat16: TQ1_BF16}[x.dtype]
+    except KeyError:
+        raise ValueError(f"libtq1 takes fp32, fp16 and bf16 here, not {x.dtype}") from None
+
+
+def _ints(x, n: int | None = None) -> int:
+    """Device address of a contiguous int32 tensor (of n elements)."""
+    import torch
+    if x.dtype != torch.int32:
+        raise ValueError(f"libtq1 takes int32 indexes, not {x.dtype}")
+    if n is not None and x.numel() != n:
+        raise ValueError(f"expected {n} values, got {x.numel()}")
+    return _addr(x)
+
+
+def _rows(x, heads: int | None, d: int, what: str) -> tuple[int, int]:
+    """Address and token stride (elements) of [t][heads][d] rows, e.g. a column range of a fused projection."""
+    if x.dim() != 3 or x.shape[2] != d or (heads is not None and x.shape[1] != heads):
+        raise ValueError(f"{what}: expected [t][{heads or 'heads'}][{d}], got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError("libtq1 takes CUDA tensors only")
+    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d):
+        raise ValueError(f"{what}: a token's heads must be contiguous")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1] * d
+
+
+def tq1_kv_cache(k, v) -> KvCache:
+    """The cache of pages k, v [n_pages][n_kv][page_size][head_dim] (fp16 or bf16): any strides, the same for
+    both, with unit stride along head_dim.  A pool kept as [n_pages][page_size][n_kv][head_dim] is passed
+    as k.transpose(1, 2), v.transpose(1, 2)."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+        raise ValueError("k and v pages: two tensors of one shape [n_pages][n_kv][page_size][head_dim], type and strides")
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("libtq1 takes CUDA tensors only")
+    if k.stride(3) != 1:
+        raise ValueError("k and v pages: unit stride along head_dim")
+    c = KvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], k.shape[3], k.stride(0), k.stride(1),
+                k.stride(2), _dtype(k))
+    c.keep = (k, v)
+    return c
+
+
+def tq1_kv_batch(page_table, q_start, kv_len) -> KvBatch:
+    """Sequences of a call: page_table [n_seqs][max_pages], q_start [n_seqs + 1], kv_len [n_seqs], int32."""
+    n, width = page_table.shape
+    b = KvBatch(_ints(page_table), _ints(q_start, n + 1), _ints(kv_len, n), n, width)
+    b.keep = (page_table, q_start, kv_len)
+    return b
+
+
+def tq1_rope_freqs(inv_freq, rot_dim: int, base: float = 10000.0, factor: float = 1.0, orig_len: float = 0.0,
+                   low: float = 1.0, high: float = 32.0, stream=None) -> None:
+    """Fill inv_freq [rot_dim/2] (fp32): plain, or stretched for contexts `factor` times longer than orig_len."""
+    if inv_freq.numel() != rot_dim // 2 or _dtype(inv_freq) != TQ1_F32:
+        raise ValueError(f"inv_freq: expected {rot_dim // 2} fp32 values")
+    _check(library().tq1_rope_freqs(_addr(inv_freq), rot_dim, base, factor, orig_len, low, high, _stream(stream)),
+           "tq1_rope_freqs")
+
+
+def tq1_rope_append(cache, batch, q, k, v, q_out, inv_freq, rot_dim: int, interleaved: bool = False,
+                    mscale: float = 1.0, positions=None, stream=None) -> None:
+    """Rotate q [t][n_q][d] into q_out and append the rotated k and the v [t][n_kv][d] to the cache's pages."""
+    t, n_q, d, n_kv = q.shape[0], q.shape[1], cache.head_dim, cache.n_kv
+    (pq, ldq), (pk, ldk), (pv, ldv) = _rows(q, None, d, "q"), _rows(k, n_kv, d, "k"), _rows(v, n_kv, d, "v")
+    if k.shape[0] != t or v.shape[0] != t or not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k and v: one type and one number of tokens")
+    if tuple(q_out.shape) != (t, n_q, d) or _dtype(q_out) != cache.dtype:
+        raise ValueError("q_out: q's shape and the cache's type")
+    if inv_freq is not None and (inv_freq.numel() != rot_dim // 2 or _dtype(inv_freq) != TQ1_F32):
+        raise ValueError(f"inv_freq: expected {rot_dim // 2} fp32 values")
+    pos = None if positions is None else _ints(positions, t)
+    _check(library().tq1_rope_append(cache, batch, pq, ldq, pk, ldk, pv, ldv, _dtype(q), _addr(q_out), t, n_q,
+                                     _addr(inv_freq), rot_dim, int(bool(interleaved)), mscale, pos, _stream(stream)),
+           "tq1_rope_append")
+
+
+def tq1_paged_attn_workspace_size(cache, t: int, n_q: int, n_seqs: int) -> int:
+    return int(library().tq1_paged_attn_workspace_size(cache, t, n_q, n_seqs))
+
+
+def tq1_paged_attn(cache, batch, q, out, scale: float, causal: bool = True, window: int = 0, ws=None,
+                   ws_bytes: int | None = None, stream=None) -> None:
+    """out [t][n_q][d] (the cache's type, or fp32) = attention of q [t][n_q][d] over the batch's pages."""
+    t, n_q, d = q.shape[0], q.shape[1], cache.head_dim
+    (pq, ldq), (po, ldo) = _rows(q, None, d, "q"), _rows(out, n_q, d, "out")
+    if out.shape[0] != t or _dtype(q) != cache.dtype or _dtype(out) not in (cache.dtype, TQ1_F32):
+        raise ValueError("q: the cache's type; out: q's shape, the cache's type or fp32")
+    wsb = ws_bytes if ws_bytes is not None else (0 if ws is None else ws.numel() * ws.element_size())
+    _check(library().tq1_paged_attn(cache, batch, pq, ldq, t, n_q, scale, int(bool(causal)), window, po, ldo,
+                                    int(_dtype(out) == TQ1_F32), _addr(ws), wsb, _stream(stream)), "tq1_paged_attn")
+
+
+def tq1_page_pool(pools, page_table, kv_len, refs, page_size: int) -> PagePool:
+    """The pools [n_pools][n_pages][...] (any type; each page contiguous) that share page_table [n_seqs][max_pages],
+    kv_len [n_seqs] and refs [n_pages] (int32)."""
+    if not pools.is_cuda or pools.dim() < 3 or not pools[0].is_contiguous():
+        raise ValueError("pools: a CUDA tensor [n_pools][n_pages][...] with contiguous pools")
+    n, width = page_table.shape
+    n_pages, size = pools.shape[1], pools.element_size()
+    page_bytes = pools[0, 0].numel() * size
+    p = PagePool(pools.data_ptr(), pools.shape[0], pools.stride(0) * size if pools.shape[0] > 1 else n_pages * page_bytes,
+                 page_bytes, n_pages, _ints(refs, n_pages), _ints(page_table), _ints(kv_len, n), n, width, page_size)
+    p.keep = (pools, page_table, kv_len, refs)
+    return p
+
+
+def tq1_pages_workspace_size(pool) -> int:
+    return int(library().tq1_pages_workspace_size(pool))
+
+
+def tq1_pages_copy(pool, src, dst, stream=None) -> None:
+    """Copy pages src[i] -> dst[i] in every pool."""
+    _check(library().tq1_pages_copy(pool, _ints(src), _ints(dst, src.numel()), src.numel(), _stream(stream)),
+           "tq1_pages_copy")
+
+
+def tq1_pages_resize(pool, seqs, new_len, ws, stream=None) -> None:
+    """Set the length of sequences seqs[i] to new_len[i]: pages are freed, given, and copied where shared."""
+    _check(library().tq1_pages_resize(pool, _ints(seqs), _ints(new_len, seqs.numel()), seqs.numel(), _addr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)), "tq1_pages_resize")
+
+
+def tq1_pages_fork(pool, parents, children, ws, stream=None) -> None:
+    """The empty sequences children[i] become copies of parents[i], sharing their full pages."""
+    _check(library().tq1_pages_fork(pool, _ints(parents), _ints(children, parents.numel()), parents.numel(), _addr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream)), "tq1_pages_fork")
+
+
+def tq1_pages_compact(pool, ws, stream=None) -> None:
+    """Move the pages in use to the lowest ids; tables and counts follow."""
+    _check(library().tq1_pages_compact(pool, _addr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "tq1_pages_compact")

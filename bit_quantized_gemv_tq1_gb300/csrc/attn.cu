@@ -1,0 +1,433 @@
+// attn.cu -- attention of each sequence's newest tokens over its paged cache,
+// few rows per kv head (decode steps).
+//
+//   O[i] = sum_j p_ij V[j],  p_ij = exp(x_ij - m_i) / l_i,  x_ij = scale q_i . K[j]
+//
+// over the keys j that row i sees.  One pass over the cache with a running
+// maximum m and sum l per row: adding keys with a larger maximum m' rescales
+// what is there by exp(m - m').  Work is divided over CTAs as kv.cuh says; a
+// tile is 16 rows (tokens x query heads of one kv head) and a block 128 keys,
+// of which each of the CTA's eight warps does 16.
+//
+// Bound: HBM, every visible key and value read once (4 d bytes per key and
+// kv head, for up to 16 rows).  So the warps are independent: each copies its
+// own keys and values (16-byte asynchronous copies into a ring of its own,
+// several blocks ahead) and keeps its own m, l and O; nothing in the loop
+// waits for another warp.  The products run on mma.sync (16 x 8 x 16): 64
+// instructions per 16 keys and warp, far from a limit here, where a
+// 128-row tensor-core tile would be at most 1/8 full.
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/tq1.h"
+#include "kv.cuh"
+#include "tq1_internal.h"
+
+namespace tq1 {
+
+namespace {
+
+constexpr int kAWarps = 8, kAThreads = 32 * kAWarps;
+constexpr int kARows = 16;                // rows of a tile (one m16 operand)
+constexpr int kWarpKeys = 16;             // keys of a block per warp
+constexpr int kABlock = kWarpKeys * kAWarps;
+
+template <int D>
+struct WarpCfg {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr uint32_t kTile = kWarpKeys * D * 2;           // one warp's keys (or values) of a block
+  static constexpr uint32_t kRing = kAWarps * kStages * 2 * kTile;
+  static constexpr uint32_t kSmem = kRing;
+  // The joining of the warps overlays the ring.
+  static_assert(kAWarps * kARows * (D + 2) * 4 <= kRing, "join buffer");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Store elements e .. e+3 of an output row.
+template <typename T>
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t tok, int head, int d, int e, float4 v) {
+  const int64_t at = tok * a.ldo + static_cast<int64_t>(head) * d + e;
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+}
+
+}  // namespace
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAThreads, 1)
+    attn_warp_kernel(const KvCache c, const KvBatch b, const AttnArgs a, const TilePlan plan, Part* parts, float* slots,
+                     unsigned* status) {
+  using C = WarpCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int g = lane >> 2, qd = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Start st = find_start<kAThreads>(plan, b, c.n_kv, cta, ctas, reinterpret_cast<int*>(smem));
+  __syncthreads();
+  if (tid < 2) parts[2 * cta + tid].rows = 0;
+  if (st.units == 0) return;
+  __syncthreads();
+
+  const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTile;
+  const float sc = a.scale * kLog2e;
+  int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
+  Seq sq = load_seq(b, seq);
+  int64_t left = st.units;
+  for (bool first_seg = true;; first_seg = false) {
+    int fb, nb;
+    tile_blocks(plan, sq, tile, fb, nb);
+    const int todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
+    const int row0 = tile * kARows, rows = min(kARows, sq.n * plan.group - row0);
+    const int pos0 = sq.len - sq.n;  // position of the sequence's first new token
+
+    // The tile's queries: fragments of a 16 x D operand, rows past the end zero.
+    uint32_t qf[D / 16][4];
+    int lo[2], hi[2];  // keys [lo, hi) that rows g and g + 8 see
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      const bool there = r < rows;
+      const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
+      const uint16_t* src = a.q + (sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[ks][h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks)) : 0u;
+        qf[ks][2 + h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8)) : 0u;
+      }
+      const int pos = pos0 + tok;
+      hi[h] = there ? (plan.causal ? min(sq.len, pos + 1) : sq.len) : 0;
+      lo[h] = plan.window ? max(0, pos - plan.window + 1) : 0;
+    }
+
+    const int key0 = (fb + blk) * kABlock + warp * kWarpKeys;  // this warp's keys: key0, key0 + 128, ...
+    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
+    const uint16_t *kbase = c.k + head * c.head_stride, *vbase = c.v + head * c.head_stride;
+    int ids = -1;  // lane i: the page of step (32 n + i), for the steps being issued
+    // Request this warp's keys and values of step i; what lies past the
+    // sequence's end, or in no page, arrives as zeros.
+    auto issue = [&](int i) {
+      if (i < todo) {
+        if ((i & 31) == 0) {
+          const int k = key0 + (i + lane) * kABlock;
+          ids = -1;
+          if (i + lane < todo && k < sq.len) {
+            ids = __ldg(table + (k >> c.page_shift));
+            if (ids < 0 || ids >= c.n_pages) {
+              ids = -1;
+              raise_status(status, kStatusBadId);
+            }
+          }
+        }
+        const int k = key0 + i * kABlock;
+        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+        const int64_t off = static_cast<int64_t>(max(page, 0)) * c.page_stride + (k & (c.page_size - 1)) * c.slot_stride;
+        const int have = page < 0 ? 0 : min(kWarpKeys, sq.len - k);
+        const uint32_t dst = ring + (i % C::kStages) * 2 * C::kTile;
+        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+#pragma unroll
+        for (int n = 0; n < kWarpKeys * kChunks / 32; ++n) {
+          const int p = n * 32 + lane, row = p / kChunks, ch = p % kChunks;
+          const bool there = row < have;
+          const int64_t at = off + (there ? row : 0) * c.slot_stride + ch * 8;
+          const uint32_t to = dst + row * D * 2 + ((ch ^ (row & 7)) << 4);
+          cp_async16(to, there ? kbase + at : c.k, there);
+          cp_async16(to + C::kTile, there ? vbase + at : c.v, there);
+        }
+      }
+      cp_commit();
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < todo; ++i) {
+      issue(i + C::kStages - 1);
+      cp_wait<C::kStages - 1>();
+      __syncwarp();
+      const int k = key0 + i * kABlock;
+      const uint32_t kt = ring + (i % C::kStages) * 2 * C::kTile, vt = kt + C::kTile;
+      float s[2][4] = {};
+      {
+        // Matrices of a K load: keys 0-7 / 8-15 by elements 0-7 / 8-15 of the step.
+        const int row = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t f[4];
+          ldsm4(kt + row * D * 2 + (((2 * ks + half) ^ (row & 7)) << 4), f);
+          mma16<T>(s[0], qf[ks], f[0], f[1]);
+          mma16<T>(s[1], qf[ks], f[2], f[3]);
+        }
+      }
+      uint32_t p[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = k + 8 * (j >> 1) + 2 * qd + (j & 1);
+          x[j] = key >= lo[h] && key < hi[h] ? s[j >> 1][2 * h + (j & 1)] * sc : -INFINITY;
+        }
+        const float mx = quad_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+        const float mn = fmaxf(m[h], mx);
+        const float base = mn == -INFINITY ? 0.0f : mn;  // no key seen yet: every weight below is exp2(-inf) = 0
+        const float keep = exp2f(m[h] - base);
+        m[h] = mn;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = exp2f(x[j] - base);
+        l[h] = l[h] * keep + ((x[0] + x[1]) + (x[2] + x[3]));
+        // The weights enter the second product as 16-bit numbers in [0, 1]
+        // (the type the matrix instruction pairs with V's); the sum stays fp32.
+        p[h] = pack2<T>(x[0], x[1]);
+        p[2 + h] = pack2<T>(x[2], x[3]);
+        if (__any_sync(0xffffffffu, keep != 1.0f)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][2 * h] *= keep;
+            o[n][2 * h + 1] *= keep;
+          }
+        }
+      }
+      {
+        // Matrices of a (transposed) V load: keys 0-7 / 8-15 of elements
+        // 0-7, then of elements 8-15.
+        const int row = lane & 15, half = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t f[4];
+          ldsm4_t(vt + row * D * 2 + (((2 * n + half) ^ (row & 7)) << 4), f);
+          mma16<T>(o[2 * n], p, f[0], f[1]);
+          mma16<T>(o[2 * n + 1], p, f[2], f[3]);
+        }
+      }
+      __syncwarp();  // the slot is refilled by the next step's copies
+    }
+    cp_wait<0>();
+    __syncthreads();
+
+    // Join the warps: every warp's m, l and O, then one thread per four
+    // elements of a row, warps in order.
+    float* jm = reinterpret_cast<float*>(smem);
+    float* jl = jm + kAWarps * kARows;
+    float* jo = jl + kAWarps * kARows;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float lsum = quad_sum(l[h]);
+      const int r = g + 8 * h;
+      if (qd == 0) {
+        jm[warp * kARows + r] = m[h];
+        jl[warp * kARows + r] = lsum;
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(jo + (warp * kARows + r) * D + 8 * n + 2 * qd) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+    }
+    __syncthreads();
+    const bool whole = blk == 0 && todo == nb;
+    const int slot = first_seg ? 2 * cta : 2 * cta + 1;
+    float* out = slots + slot * join_slot_floats(kARows, D);
+    for (int e = tid; e < rows * (D / 4); e += kAThreads) {
+      const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAWarps; ++w) mx = fmaxf(mx, jm[w * kARows + r]);
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      float lt = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kAWarps; ++w) {
+        const float f = exp2f(jm[w * kARows + r] - base);
+        lt += f * jl[w * kARows + r];
+        const float4 x = *reinterpret_cast<const float4*>(jo + (w * kARows + r) * D + col);
+        v.x += f * x.x;
+        v.y += f * x.y;
+        v.z += f * x.z;
+        v.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);  // a row that sees nothing is zero
+        const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
+        store4<T>(a, sq.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+      } else {
+        if (col == 0) {
+          out[r] = mx;
+          out[kARows + r] = lt;
+        }
+        *reinterpret_cast<float4*>(out + 2 * kARows + r * D + col) = v;
+      }
+    }
+    if (!whole && tid == 0) {
+      Part& p = parts[slot];
+      p.head = head;
+      p.q0 = sq.q0;
+      p.row0 = row0;
+      p.starts = blk == 0;
+      p.ends = blk + todo == nb;
+      p.rows = rows;
+    }
+    left -= todo;
+    if (left == 0) break;
+    __syncthreads();
+    next_tile(plan, b, head, seq, tile, sq);
+    blk = 0;
+  }
+}
+
+// Join the parts of the tiles that several CTAs did.  CTA (c, y) takes the
+// tile whose first part CTA c of the attention kernel left (if any) and the
+// y-th share of its rows; the parts that follow are the first ones of CTAs
+// c + 1, c + 2, ... up to the one that ends the tile.  Fixed order: the same
+// sums every time.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+    attn_join_kernel(const AttnArgs a, int slot_rows, int group, const Part* parts, const float* slots, int ctas) {
+  pdl_wait();
+  const int c = blockIdx.x;
+  int slot = -1;
+  for (int i = 0; i < 2; ++i) {
+    const Part& p = parts[2 * c + i];
+    if (p.rows > 0 && p.starts && !p.ends) slot = 2 * c + i;
+  }
+  if (slot < 0) return;
+  const Part p = parts[slot];
+  int last = c + 1;
+  while (last < ctas && !parts[2 * last].ends) ++last;
+  const size_t sf = join_slot_floats(slot_rows, D);
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < p.rows * (D / 4); e += gridDim.y * blockDim.x) {
+    const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+    const float* s = slots + slot * sf;
+    float m = s[r], l = s[slot_rows + r];
+    float4 v = *reinterpret_cast<const float4*>(s + 2 * slot_rows + static_cast<size_t>(r) * D + col);
+#pragma unroll 4
+    for (int k = c + 1; k <= last && k < ctas; ++k) {
+      s = slots + 2 * k * sf;
+      const float mk = s[r], lk = s[slot_rows + r];
+      const float4 x = *reinterpret_cast<const float4*>(s + 2 * slot_rows + static_cast<size_t>(r) * D + col);
+      const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.0f : mn;
+      const float f0 = exp2f(m - base), f1 = exp2f(mk - base);
+      m = mn;
+      l = l * f0 + lk * f1;
+      v.x = v.x * f0 + x.x * f1;
+      v.y = v.y * f0 + x.y * f1;
+      v.z = v.z * f0 + x.z * f1;
+      v.w = v.w * f0 + x.w * f1;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    const int tok = (p.row0 + r) / group, qh = p.head * group + (p.row0 + r) - tok * group;
+    store4<T>(a, p.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+  }
+}
+
+namespace {
+
+int attn_ctas() { return device_info().num_sms; }
+
+template <typename T, int D>
+int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status, cudaStream_t s) {
+  using C = WarpCfg<D>;
+  const DeviceInfo& di = device_info();
+  static std::atomic<bool> configured[64];  // per device (racing threads configure twice: idempotent)
+  if (di.device < 0 || di.device >= 64) return TQ1_ERR_CUDA;
+  if (!configured[di.device].load(std::memory_order_acquire)) {
+    if (!cuda_ok(cudaFuncSetAttribute(attn_warp_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(C::kSmem))))
+      return TQ1_ERR_CUDA;
+    configured[di.device].store(true, std::memory_order_release);
+  }
+  const int ctas = attn_ctas();
+  Part* parts = static_cast<Part*>(ws);
+  float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + join_parts_bytes(ctas));
+  TilePlan plan = {kARows, kABlock, a.n_q / c.n_kv, a.causal, a.window};
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kAThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (!cuda_ok(cudaLaunchKernelEx(&cfg, attn_warp_kernel<T, D>, c, b, a, plan, parts, slots, status)))
+    return TQ1_ERR_CUDA;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 2);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a, kARows, plan.group, static_cast<const Part*>(parts),
+                                    static_cast<const float*>(slots), ctas))
+             ? TQ1_OK
+             : TQ1_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t attn_workspace_bytes(const KvCache& c, int64_t t, int64_t n_q, int64_t n_seqs) {
+  const int ctas = attn_ctas();
+  const size_t b = join_parts_bytes(ctas) + 2 * static_cast<size_t>(ctas) * join_slot_floats(kARows, c.d) * sizeof(float);
+  return (b + 255) & ~size_t(255);
+}
+
+int launch_attn(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status, cudaStream_t s) {
+  if (c.d == 128)
+    return c.dtype == kBf16 ? launch_warp<__nv_bfloat16, 128>(c, b, a, ws, status, s)
+                            : launch_warp<__half, 128>(c, b, a, ws, status, s);
+  return c.dtype == kBf16 ? launch_warp<__nv_bfloat16, 64>(c, b, a, ws, status, s)
+                          : launch_warp<__half, 64>(c, b, a, ws, status, s);
+}
+
+}  // namespace tq1

@@ -6,6 +6,7 @@
 
 #include "../../include/tq1.h"
 #include "tq1_device.cuh"
+#include "kv_internal.h"
 #include "tq1_internal.h"
 
 // Device status word of this library (see tq1_sync_status).  Kernels get its
@@ -90,6 +91,8 @@ int check_mmv_shape(int64_t n, int64_t k, int64_t t) {
 }
 }  // namespace
 
+unsigned* status_word() { return status_ptr(); }
+
 bool cuda_ok(cudaError_t err) {
   if (err == cudaSuccess) return true;
   snprintf(g_last_err, sizeof(g_last_err), "%s: %s", cudaGetErrorName(err), cudaGetErrorString(err));
@@ -119,7 +122,8 @@ const char* tq1_status_string(int status) {
     case TQ1_ERR_WORKSPACE: return "workspace too small";
     case TQ1_ERR_CUDA: return "CUDA runtime error";
     case TQ1_ERR_TIMEOUT: return "a kernel timed out waiting for a transfer";
-    case TQ1_ERR_BAD_ID: return "routing id outside [0, n_experts)";
+    case TQ1_ERR_BAD_ID: return "routing, page or sequence id out of range";
+    case TQ1_ERR_NO_PAGES: return "no free pages, or no room in a page-table row";
     default: return "unknown status";
   }
 }
@@ -435,6 +439,7 @@ int tq1_sync_status(void* stream) {
   if (!cuda_ok(cudaMemcpy(st, &zero, sizeof(zero), cudaMemcpyHostToDevice))) return TQ1_ERR_CUDA;
   if (v & kStatusTimeout) return TQ1_ERR_TIMEOUT;
   if (v & kStatusBadId) return TQ1_ERR_BAD_ID;
+  if (v & kStatusNoPages) return TQ1_ERR_NO_PAGES;
   return TQ1_OK;
 }
 

@@ -1,0 +1,248 @@
+// kv.cuh -- the paged key/value cache as the kernels see it, 16-bit element
+// helpers, and the division of an attention call's work among its CTAs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv_internal.h"
+#include "tq1_device.cuh"
+
+namespace tq1 {
+
+// ------------------------------------------------------ 16-bit elements --
+// Two fp32 values to two 16-bit elements (round to nearest), the first in the
+// low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+
+// --------------------------------------------------------- the sequences --
+// New tokens [q0, q0 + n) and cache length of one sequence.  The arrays are
+// device data the host has not seen, so they are clamped to what exists: no
+// index formed from them leaves the call's tensors.
+struct Seq {
+  int q0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
+  Seq r;
+  int q0 = __ldg(b.q_start + s), q1 = __ldg(b.q_start + s + 1);
+  r.len = min(max(__ldg(b.kv_len + s), 0), b.max_len);
+  q0 = min(max(q0, 0), b.t);
+  q1 = min(max(q1, q0), b.t);
+  r.q0 = q0;
+  r.n = q1 - q0;
+  return r;
+}
+
+// ------------------------------------------------- division of attention --
+// The (token, query head of the group) pairs of one sequence and one kv head
+// are its rows, row = token * group + head, cut into tiles of `rows` rows.
+// A tile reads the cache in blocks of `block` keys, from the first key any
+// of its rows sees to the last.  The call's work is the list of (kv head,
+// sequence, tile, block), in that order; CTA c of C does the units
+// [W c / C, W (c+1) / C) of the W in the list.  So every CTA has the same
+// work to one unit whatever the sequences' lengths are, and only the tiles at
+// a CTA's two ends are shared: their parts are joined afterwards.
+struct TilePlan {
+  int rows, block, group, causal, window;
+};
+
+// Blocks of one tile: the first one and how many.  A tile whose rows see
+// nothing has one block (it is masked whole; its rows come out as zeros).
+__device__ __forceinline__ void tile_blocks(const TilePlan& p, const Seq& s, int tile, int& first, int& count) {
+  const int r0 = tile * p.rows, r1 = min(r0 + p.rows, s.n * p.group);
+  const int tok0 = r0 / p.group, tok1 = (r1 - 1) / p.group;
+  const int pos0 = s.len - s.n + tok0, pos1 = s.len - s.n + tok1;
+  const int hi = p.causal ? min(s.len, pos1 + 1) : s.len;
+  const int lo = p.window ? max(0, pos0 - p.window + 1) : 0;
+  first = lo / p.block;
+  count = max(1, (hi + p.block - 1) / p.block - first);
+  if (hi <= lo) count = 1;
+}
+__device__ __forceinline__ int seq_tiles(const TilePlan& p, const Seq& s) {
+  return (s.n * p.group + p.rows - 1) / p.rows;
+}
+
+// Inclusive sum over the block's threads in thread order; `s_warp` holds one
+// int per warp.  Returns the inclusive sum, and the block's total in `total`.
+template <int NT>
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // s_warp may still be read from the call before
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int x = s_warp[w];
+    if (w < warp) before += x;
+    total += x;
+  }
+  return v + before;
+}
+
+// Where CTA `cta` of `ctas` begins and how much it does.
+struct Start {
+  int head, seq, tile, block;  // first unit
+  int64_t units;               // units of this CTA (0: none)
+};
+
+constexpr int kMaxSeqs = 8192;
+
+// Called by all NT threads.  `s_nb`: at least n_seqs ints of shared memory,
+// free again when the call returns.
+template <int NT>
+__device__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int* s_nb) {
+  __shared__ int s_warp[NT / 32];
+  __shared__ int s_big[2], s_hit[3];
+  // Blocks of each sequence: one thread per sequence of few tiles, all
+  // threads for one of many.
+  int mine = 0;
+  for (int base = 0; base < b.n_seqs; base += NT) {
+    const int s = base + threadIdx.x;
+    int nb = 0;
+    if (s < b.n_seqs) {
+      const Seq q = load_seq(b, s);
+      const int tiles = seq_tiles(p, q);
+      if (tiles <= 8) {
+        for (int i = 0; i < tiles; ++i) {
+          int f, c;
+          tile_blocks(p, q, i, f, c);
+          nb += c;
+        }
+      } else {
+        nb = -1;
+      }
+      s_nb[s] = nb;
+    }
+    mine |= nb < 0;
+  }
+  if (__syncthreads_or(mine)) {
+    for (int s = 0; s < b.n_seqs; ++s) {
+      if (s_nb[s] >= 0) continue;  // the same for every thread
+      const Seq q = load_seq(b, s);
+      const int tiles = seq_tiles(p, q);
+      int nb = 0;
+      for (int i = threadIdx.x; i < tiles; i += NT) {
+        int f, c;
+        tile_blocks(p, q, i, f, c);
+        nb += c;
+      }
+      int total;
+      (void)block_scan<NT>(nb, s_warp, total);
+      if (threadIdx.x == 0) s_nb[s] = total;
+      __syncthreads();
+    }
+  }
+  int64_t all = 0;  // blocks of one kv head
+  for (int base = 0; base < b.n_seqs; base += NT) {
+    const int s = base + threadIdx.x;
+    int total;
+    (void)block_scan<NT>(s < b.n_seqs ? s_nb[s] : 0, s_warp, total);
+    all += total;
+  }
+  Start r;
+  const int64_t work = all * n_kv;
+  const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
+  const int64_t u0 = cta < used ? work * cta / used : 0, u1 = cta < used ? work * (cta + 1) / used : 0;
+  r.units = u1 - u0;
+  r.head = r.seq = r.tile = r.block = 0;
+  if (r.units == 0) return r;  // the same for every thread
+  r.head = static_cast<int>(u0 / all);
+  int rem = static_cast<int>(u0 - r.head * all);
+  int before = 0;
+  for (int base = 0; base < b.n_seqs; base += NT) {
+    const int s = base + threadIdx.x;
+    const int v = s < b.n_seqs ? s_nb[s] : 0;
+    int total;
+    const int end = before + block_scan<NT>(v, s_warp, total);
+    if (rem >= end - v && rem < end) {
+      s_big[0] = s;
+      s_big[1] = rem - (end - v);
+    }
+    before += total;
+    if (before > rem) break;  // the same for every thread
+  }
+  __syncthreads();
+  r.seq = s_big[0];
+  rem = s_big[1];
+  const Seq q = load_seq(b, r.seq);
+  const int tiles = seq_tiles(p, q);
+  before = 0;
+  for (int base = 0; base < tiles; base += NT) {
+    const int i = base + threadIdx.x;
+    int f = 0, v = 0, total;
+    if (i < tiles) tile_blocks(p, q, i, f, v);
+    const int end = before + block_scan<NT>(v, s_warp, total);
+    if (rem >= end - v && rem < end) {
+      s_hit[0] = i;
+      s_hit[1] = rem - (end - v);
+    }
+    before += total;
+    if (before > rem) break;
+  }
+  __syncthreads();
+  r.tile = s_hit[0];
+  r.block = s_hit[1];
+  return r;
+}
+
+// The next tile after (head, seq, tile); there is one, since the CTA has
+// units left.
+__device__ __forceinline__ void next_tile(const TilePlan& p, const KvBatch& b, int& head, int& seq, int& tile, Seq& q) {
+  if (++tile < seq_tiles(p, q)) return;
+  tile = 0;
+  for (int i = 0; i <= b.n_seqs; ++i) {  // at most once around: sequences without new tokens have no tiles
+    if (++seq == b.n_seqs) {
+      seq = 0;
+      ++head;
+    }
+    q = load_seq(b, seq);
+    if (q.n > 0) return;
+  }
+}
+
+// ------------------------------------------------------------ the joining --
+// What a CTA left of a tile it did not do alone (its first or its last):
+// rows of m, l and unnormalised O in the workspace, described by a Part.
+struct Part {
+  int head, q0, row0, rows;  // kv head, first token of the sequence, first row of the tile, rows (0: no part)
+  int starts, ends;          // whether the part has the tile's first / last block
+  int pad[2];
+};
+
+// Workspace of `ctas` CTAs: their parts, then two slots each of rows * (d + 2)
+// floats: m [rows], l [rows], O [rows][d].
+inline __host__ __device__ size_t join_parts_bytes(int ctas) { return static_cast<size_t>(ctas) * 2 * sizeof(Part); }
+inline __host__ __device__ size_t join_slot_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+
+}  // namespace tq1

@@ -1,0 +1,223 @@
+// rope.cu -- rotary positions, and the append of rotated keys and of values
+// to the paged cache.
+//
+// A head's first `rot` elements are rot/2 pairs; pair i of the token at
+// position p turns by the angle a = p * f_i (f: inv_freq):
+//   x' = m (x cos a - y sin a),   y' = m (x sin a + y cos a)
+// with (x, y) = elements (i, i + rot/2), or (2i, 2i + 1) when interleaved;
+// the head's other elements are copied.  q goes to q_out, k and v to the slot
+// that the token's position in its sequence names, so a projection's output
+// is read once and every result written once.
+//
+// The angle: p f_i reaches 10^5 and more radians, where an fp32 product is
+// already off by 0.01.  It is formed in fp64, in half turns, and reduced
+// there; the rest, below one half turn, goes to sincospif.  Four fp64
+// operations per angle, and one angle serves all heads of a token.
+//
+// Bound: HBM for chunks (6 bytes per value in, out); latency for a step.
+// A thread does 8 elements of one head: two 4-element halves of the "half"
+// layout (4 pairs), or 8 neighbours, so that a warp's accesses are whole
+// 128-byte lines (16-byte loads, 8- or 16-byte stores).
+#include "../../include/tq1.h"
+#include "kv.cuh"
+#include "tq1_internal.h"
+
+namespace tq1 {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kMaxRotPairs = 128;  // head_dim <= 256
+
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = x.z;
+  v[3] = x.w;
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
+  const uint2 x = __ldcs(reinterpret_cast<const uint2*>(p));
+  const float2 a = unpack2<T>(x.x), b = unpack2<T>(x.y);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+
+// One CTA: `per` tokens from blockIdx.x * per on, and of each token's items
+// (groups of 8 elements of the q, k and v heads) those of part blockIdx.y of
+// gridDim.y.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache c, const KvBatch b, const RopeArgs a,
+                                                                   int per, unsigned* status) {
+  __shared__ float2 s_cs[4][kMaxRotPairs];
+  __shared__ int s_seq[4], s_pos[4], s_page[4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tok0 = blockIdx.x * per;
+  pdl_wait();
+  // The sequence of each token, its position and its page: a warp per token.
+  if (warp < per) {
+    const int tok = tok0 + warp;
+    int seq = -1, pos = 0, page = -1;
+    if (tok < b.t) {
+      int count = 0;  // sequences that end at or before this token
+      for (int s = lane; s < b.n_seqs; s += 32) count += __ldg(b.q_start + s + 1) <= tok;
+      count = __reduce_add_sync(0xffffffffu, count);
+      if (count < b.n_seqs && __ldg(b.q_start + count) <= tok) {
+        seq = count;
+        pos = __ldg(b.kv_len + seq) - (__ldg(b.q_start + seq + 1) - tok);
+        if (pos >= 0 && pos < b.max_len) {
+          page = __ldg(b.table + static_cast<int64_t>(seq) * b.max_pages + (pos >> c.page_shift));
+          if (page < 0 || page >= c.n_pages) page = -1;
+        }
+        if (page < 0 && lane == 0 && blockIdx.y == 0) raise_status(status, kStatusBadId);
+      }
+    }
+    if (lane == 0) {
+      s_seq[warp] = seq;
+      s_pos[warp] = pos;
+      s_page[warp] = page;
+    }
+  }
+  __syncthreads();
+  const int pairs = a.rot >> 1;
+  for (int i = tid; i < per * pairs; i += kRopeThreads) {
+    const int w = i / pairs, p = i - w * pairs;
+    if (s_seq[w] < 0) continue;
+    const int pos = a.positions ? __ldg(a.positions + tok0 + w) : s_pos[w];
+    double half_turns = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + p)) * 0.31830988618379067154;
+    half_turns -= 2.0 * rint(0.5 * half_turns);
+    float sn, cs;
+    sincospif(static_cast<float>(half_turns), &sn, &cs);
+    s_cs[w][p] = make_float2(cs * a.mscale, sn * a.mscale);
+  }
+  __syncthreads();
+  const int groups = c.d >> 3, rotg = a.rot >> 3;
+  const int heads = a.n_q + 2 * c.n_kv;
+  const int items = heads * groups;
+  const int from = static_cast<int>(static_cast<int64_t>(items) * blockIdx.y / gridDim.y);
+  const int to = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.y + 1) / gridDim.y);
+  const int span = to - from;
+  for (int i = tid; i < per * span; i += kRopeThreads) {
+    const int w = i / span, item = from + i - w * span;
+    if (s_seq[w] < 0) continue;
+    const int tok = tok0 + w;
+    const int head = item / groups, grp = item - head * groups;
+    const bool is_q = head < a.n_q, is_v = head >= a.n_q + c.n_kv;
+    const TI* src;
+    TO* dst;
+    if (is_q) {
+      src = static_cast<const TI*>(a.q) + tok * a.ldq + static_cast<int64_t>(head) * c.d;
+      dst = reinterpret_cast<TO*>(a.q_out) + (static_cast<int64_t>(tok) * a.n_q + head) * c.d;
+    } else {
+      if (s_page[w] < 0) continue;
+      const int h = is_v ? head - a.n_q - c.n_kv : head - a.n_q;
+      src = is_v ? static_cast<const TI*>(a.v) + tok * a.ldv : static_cast<const TI*>(a.k) + tok * a.ldk;
+      src += static_cast<int64_t>(h) * c.d;
+      dst = reinterpret_cast<TO*>(is_v ? c.v : c.k) + s_page[w] * c.page_stride + h * c.head_stride +
+            (s_pos[w] & (c.page_size - 1)) * c.slot_stride;
+    }
+    const bool turn = !is_v && grp < rotg;
+    // Elements e0 .. e0+3 and e1 .. e1+3 of the head.
+    const bool halves = turn && !a.interleaved;
+    const int e0 = halves ? 4 * grp : 8 * grp, e1 = halves ? e0 + pairs : e0 + 4;
+    float x[4], y[4];
+    load4(src + e0, x);
+    load4(src + e1, y);
+    if (halves) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 cs = s_cs[w][e0 + j];
+        const float u = x[j] * cs.x - y[j] * cs.y;
+        y[j] = x[j] * cs.y + y[j] * cs.x;
+        x[j] = u;
+      }
+    } else if (turn) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 c0 = s_cs[w][(e0 >> 1) + j], c1 = s_cs[w][(e1 >> 1) + j];
+        float u = x[2 * j] * c0.x - x[2 * j + 1] * c0.y;
+        x[2 * j + 1] = x[2 * j] * c0.y + x[2 * j + 1] * c0.x;
+        x[2 * j] = u;
+        u = y[2 * j] * c1.x - y[2 * j + 1] * c1.y;
+        y[2 * j + 1] = y[2 * j] * c1.y + y[2 * j + 1] * c1.x;
+        y[2 * j] = u;
+      }
+    }
+    const uint2 lo = make_uint2(pack2<TO>(x[0], x[1]), pack2<TO>(x[2], x[3]));
+    const uint2 hi = make_uint2(pack2<TO>(y[0], y[1]), pack2<TO>(y[2], y[3]));
+    if (halves) {
+      *reinterpret_cast<uint2*>(dst + e0) = lo;
+      *reinterpret_cast<uint2*>(dst + e1) = hi;
+    } else {
+      *reinterpret_cast<uint4*>(dst + e0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+}
+
+// f_i = theta_i ((1 - g) / factor + g), theta_i = base^(-2i / rot), where g
+// ramps from 0 to 1 with the turns orig_len theta_i / 2 pi that the pair makes
+// over the original context, between `low` and `high` turns: fast pairs keep
+// their frequency, slow ones are stretched by the factor.  fp64, rounded once.
+__global__ void rope_freqs_kernel(float* inv_freq, int pairs, double base, double factor, double orig_len, double low,
+                                  double high) {
+  pdl_wait();
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    const double theta = pow(base, -static_cast<double>(i) / pairs);
+    double g = 1.0;
+    if (factor != 1.0) {
+      const double turns = orig_len * theta * 0.15915494309189533577;
+      g = high > low ? (turns - low) / (high - low) : (turns >= high ? 1.0 : 0.0);
+      g = fmin(fmax(g, 0.0), 1.0);
+    }
+    inv_freq[i] = static_cast<float>(theta * ((1.0 - g) / factor + g));
+  }
+}
+
+template <typename TI, typename TO>
+int launch(const KvCache& c, const KvBatch& b, const RopeArgs& a, unsigned* status, cudaStream_t s) {
+  // Four tokens a CTA share its start; while that leaves SMs without a CTA,
+  // one token a CTA, its items split over as many CTAs as keep one item a
+  // thread.
+  const int items = (a.n_q + 2 * c.n_kv) * (c.d >> 3);
+  const int sms = device_info().num_sms;
+  const int per = b.t >= 8 * sms ? 4 : 1;
+  const int64_t gx = (static_cast<int64_t>(b.t) + per - 1) / per;
+  int gy = 1;
+  while (gy < 16 && gx * gy < 2 * sms && items > gy * kRopeThreads) ++gy;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, rope_append_kernel<TI, TO>, c, b, a, per, status)) ? TQ1_OK : TQ1_ERR_CUDA;
+}
+
+template <typename TO>
+int launch_out(const KvCache& c, const KvBatch& b, const RopeArgs& a, unsigned* status, cudaStream_t s) {
+  switch (a.in_dtype) {
+    case kF16: return launch<__half, TO>(c, b, a, status, s);
+    case kBf16: return launch<__nv_bfloat16, TO>(c, b, a, status, s);
+    default: return launch<float, TO>(c, b, a, status, s);
+  }
+}
+
+}  // namespace
+
+int launch_rope_append(const KvCache& c, const KvBatch& b, const RopeArgs& a, unsigned* status, cudaStream_t s) {
+  return c.dtype == kBf16 ? launch_out<__nv_bfloat16>(c, b, a, status, s) : launch_out<__half>(c, b, a, status, s);
+}
+
+int launch_rope_freqs(float* inv_freq, int rot, double base, double factor, double orig_len, double low, double high,
+                      cudaStream_t s) {
+  rope_freqs_kernel<<<1, 128, 0, s>>>(inv_freq, rot / 2, base, factor, orig_len, low, high);
+  return cuda_ok(cudaGetLastError()) ? TQ1_OK : TQ1_ERR_CUDA;
+}
+
+}  // namespace tq1

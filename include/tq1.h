@@ -1,6 +1,7 @@
 /*
- * tq1.h -- C ABI of libtq1: ternary TQ1_0 weights x Q8_1 activations on
- * NVIDIA GB300 (sm_103a).
+ * tq1.h -- C ABI of libtq1: ternary TQ1_0 weights x Q8_1 activations, and the
+ * decoder layer between such products (rotary positions, paged key/value
+ * cache, attention), on NVIDIA GB300 (sm_103a).
  *
  * Formats (PrismML-Eng/llama.cpp issue #139, "Current behavior": five trits
  * per byte in base 3, chunk c of a 256-element block reading digit c of
@@ -69,7 +70,8 @@ enum tq1_status {
   TQ1_ERR_WORKSPACE = -5,   /* workspace too small */
   TQ1_ERR_CUDA = -6,        /* a CUDA runtime call failed */
   TQ1_ERR_TIMEOUT = -7,     /* a kernel gave up waiting on a transfer (device status) */
-  TQ1_ERR_BAD_ID = -8       /* a routing id was outside [0, n_experts) (device status) */
+  TQ1_ERR_BAD_ID = -8,      /* a routing, page or sequence id was out of range (device status) */
+  TQ1_ERR_NO_PAGES = -9     /* no free pages, or no room in a page-table row (device status) */
 };
 
 /* Text for a status code (static storage).  No passage: a convention of this
@@ -326,8 +328,9 @@ int tq1_mmv_id_noalloc(const void* expert_blocks, int64_t n_experts, const void*
 
 /*
  * Synchronise `stream`, then return and clear the device status word:
- * TQ1_OK, TQ1_ERR_TIMEOUT or TQ1_ERR_BAD_ID (or TQ1_ERR_CUDA if the stream
- * itself reported an error).  No passage: a convention of this library (the
+ * TQ1_OK, TQ1_ERR_TIMEOUT, TQ1_ERR_BAD_ID or TQ1_ERR_NO_PAGES, the first of
+ * them that was raised in this order (or TQ1_ERR_CUDA if the stream itself
+ * reported an error).  No passage: a convention of this library (the
  * pages define no error reporting).
  */
 int tq1_sync_status(void* stream);
@@ -398,6 +401,180 @@ int tq2_mmv_id(const void* expert_blocks, int64_t n_experts, const void* q8, con
                int64_t n, int64_t k, int64_t t, int64_t top_k, void* ws, size_t ws_bytes, void* stream);
 int tq2_mmv_id_slots(const void* expert_blocks, int64_t n_experts, const void* q8, const int32_t* ids, float* y,
                      int64_t n, int64_t k, int64_t t, int64_t top_k, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The decoder layer between the projections: rotary positions, a paged
+ * key/value cache, the attention that reads it, and its page bookkeeping.
+ * A layer's step is: tq1_mmv (q, k, v) -> tq1_rope_append -> tq1_paged_attn
+ * (fp32 output) -> q8_1_quantize_acts -> tq1_mmv_add (output projection).
+ *
+ * The cache keeps keys and values in pages of page_size slots (one slot per
+ * token and kv head, head_dim 16-bit elements).  Page p, kv head h, slot s
+ * starts at element p * page_stride + h * head_stride + s * slot_stride of k
+ * and of v; only the head_dim elements of a slot have to be contiguous.
+ * Slot j of sequence s (its token at position j) is slot j % page_size of
+ * page page_table[s][j / page_size].
+ *
+ * Conventions beside those at the top of this file:
+ *   - page_table, q_start, kv_len and the other index arrays are int32 in
+ *     device memory (4-byte aligned; refs 16-byte) and are read when the
+ *     kernels run.  Whatever they hold, no kernel leaves the tensors of the
+ *     call: lengths are cut to what the page table addresses, and a page or
+ *     sequence id out of range is skipped and sets TQ1_ERR_BAD_ID in the
+ *     device status.
+ *   - The structs are read during the call only; the caller may reuse them.
+ *   - Strides are multiples of 8 elements (16 bytes), page_size is 16, 32,
+ *     64, 128 or 256, head_dim a multiple of 8 up to 256; n_seqs <= 8192,
+ *     max_pages <= 2^20, t <= 2^24.
+ * ------------------------------------------------------------------------ */
+enum tq1_dtype { TQ1_F32 = 0, TQ1_F16 = 1, TQ1_BF16 = 2 };
+
+typedef struct tq1_kv_cache {
+  void* k;              /* 16-byte aligned */
+  void* v;
+  int64_t n_pages, n_kv, page_size, head_dim;
+  int64_t page_stride, head_stride, slot_stride; /* elements */
+  int32_t dtype;        /* TQ1_F16 or TQ1_BF16 */
+} tq1_kv_cache;
+
+/* A batch of sequences: sequence s has the call's tokens q_start[s] ..
+ * q_start[s + 1] - 1 (none is fine) and kv_len[s] tokens in all, these
+ * included; so its token i stands at position kv_len[s] - (q_start[s + 1] -
+ * i).  Tokens from q_start[n_seqs] on belong to no sequence and are left
+ * alone. */
+typedef struct tq1_kv_batch {
+  const int32_t* page_table; /* [n_seqs][max_pages] */
+  const int32_t* q_start;    /* [n_seqs + 1], ascending */
+  const int32_t* kv_len;     /* [n_seqs] */
+  int64_t n_seqs, max_pages;
+} tq1_kv_batch;
+
+/* The pools of a cache (e.g. the keys and the values of every layer) that
+ * share one set of tables: pool i's page p is the page_bytes bytes at base +
+ * i * pool_stride + p * page_bytes (both multiples of 16).  refs[p] is how
+ * many sequences hold page p; a page is free exactly when it is 0. */
+typedef struct tq1_page_pool {
+  void* base;
+  int64_t n_pools, pool_stride, page_bytes, n_pages;
+  int32_t* refs;        /* [n_pages] */
+  int32_t* page_table;  /* [n_seqs][max_pages], -1 where there is no page */
+  int32_t* kv_len;      /* [n_seqs], 0: the sequence is empty */
+  int64_t n_seqs, max_pages, page_size;
+} tq1_page_pool;
+
+/*
+ * Inverse frequencies of rotary positions, inv_freq[i] for the rot_dim / 2
+ * rotated pairs: theta_i ((1 - g) / factor + g), theta_i = base^(-2i/rot_dim).
+ * factor == 1 gives theta_i.  For contexts `factor` times longer than the
+ * orig_len positions a model was trained on, g ramps from 0 (stretched by the
+ * factor) to 1 (kept) as the turns orig_len theta_i / 2 pi of a pair go from
+ * `low` to `high`; low = high = INFINITY stretches all pairs alike.  fp64,
+ * rounded once.  inv_freq: fp32 [rot_dim / 2], device; rot_dim even, <= 256.
+ * No passage: a convention of this library.
+ */
+int tq1_rope_freqs(float* inv_freq, int64_t rot_dim, double base, double factor, double orig_len, double low,
+                   double high, void* stream);
+
+/*
+ * Rotary positions and cache append.  For every token of the batch: the first
+ * rot_dim elements of each q and k head turn by the token's position, the
+ * rotated q goes to q_out, the rotated k and the v to the token's cache slot.
+ * Pair i, (x, y) = elements (i, i + rot_dim/2), or (2i, 2i + 1) when
+ * interleaved != 0, becomes mscale * (x cos a - y sin a, x sin a + y cos a)
+ * with a = position * inv_freq[i] (formed in fp64); elements from rot_dim on
+ * are copied.  rot_dim is a multiple of 8, 0 <= rot_dim <= head_dim.
+ *   q: [t][n_q][head_dim], k and v: [t][n_kv][head_dim], all of type in_dtype
+ *      (TQ1_F32, TQ1_F16 or TQ1_BF16), tokens ldq / ldk / ldv elements apart
+ *      (multiples of 4): column ranges of one fused projection will do
+ *   q_out: [t][n_q][head_dim] of the cache's type, contiguous
+ *   positions: int32 [t] (device) to turn by instead of the tokens' positions
+ *      in their sequences, or NULL; the slots stay the sequences'
+ * Values are rounded once, to the cache's type.  A token whose slot is outside
+ * its page-table row, or in no valid page, is not appended (its q row is
+ * written) and sets TQ1_ERR_BAD_ID.
+ * No passage: a convention of this library.
+ */
+int tq1_rope_append(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const void* q, int64_t ldq, const void* k,
+                    int64_t ldk, const void* v, int64_t ldv, int in_dtype, void* q_out, int64_t t, int64_t n_q,
+                    const float* inv_freq, int64_t rot_dim, int interleaved, float mscale, const int32_t* positions,
+                    void* stream);
+
+/* Workspace bytes tq1_paged_attn needs for t tokens of n_seqs sequences with
+ * n_q query heads (0: invalid arguments).  No passage: a convention of this
+ * library. */
+size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64_t n_q, int64_t n_seqs);
+
+/*
+ * Attention of the batch's tokens over their sequences' pages:
+ *   out[i][h] = sum_j p_j V[j],  p = softmax over the visible j of scale * q[i][h] . K[j]
+ * with K, V of kv head h / (n_q / n_kv).  Visible to the token at position p
+ * are the slots j < kv_len with j <= p (causal != 0) and j > p - window
+ * (window > 0).  A row that sees nothing is 0.  One call serves decode steps
+ * (one token per sequence), prompt chunks and any mix of them.
+ *   q: [t][n_q][head_dim] of the cache's type, tokens ldq elements apart
+ *   out: [t][n_q][head_dim] of the cache's type, or fp32 when out_f32 != 0
+ *      (what q8_1_quantize_acts takes), tokens ldo elements apart; rows of
+ *      tokens that belong to no sequence are left alone
+ *   ws: device, 16-byte aligned, tq1_paged_attn_workspace_size() bytes
+ *      (TQ1_ERR_WORKSPACE otherwise), in use until the call's kernels finish
+ * Scores, maxima, sums and outputs are accumulated in fp32; the weights p
+ * enter the second product as 16-bit numbers of the cache's type.  Slots at
+ * or past kv_len may hold anything, NaN included; a value that is not finite
+ * in a slot below kv_len reaches every row of the tiles that read it.
+ * Deterministic.  head_dim 64 or 128, n_q a multiple of n_kv, at most 128
+ * query heads per kv head (TQ1_ERR_UNSUPPORTED otherwise); scale > 0;
+ * ldq, ldo multiples of 8.
+ * No passage: a convention of this library.
+ */
+int tq1_paged_attn(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const void* q, int64_t ldq, int64_t t,
+                   int64_t n_q, float scale, int causal, int64_t window, void* out, int64_t ldo, int out_f32, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tq1_pages_resize, _fork and _compact on this pool (0:
+ * invalid arguments).  No passage: a convention of this library. */
+size_t tq1_pages_workspace_size(const tq1_page_pool* pool);
+
+/*
+ * Copy pages src[i] -> dst[i], i < n, in every pool.  No destination may be a
+ * source or occur twice (the copies run in no order); tables and counts are
+ * left alone.  No passage: a convention of this library.
+ */
+int tq1_pages_copy(const tq1_page_pool* pool, const int32_t* src, const int32_t* dst, int64_t n, void* stream);
+
+/*
+ * Set the length of sequences seqs[i] (distinct) to new_len[i], i < n <=
+ * n_seqs.  First all that shrink let their pages past the new length go (new
+ * length 0 frees a sequence).  Then those that grow get the lowest free
+ * pages, in the order of the arguments; one whose last page is partly filled
+ * and held by other sequences too first gets a copy of that page for itself
+ * (free pages and holders as they stand when all shrinking is done).  From
+ * the first sequence on that the free pages do not suffice for, none grows;
+ * these keep their length and TQ1_ERR_NO_PAGES is set, as it is for a length
+ * that is negative or beyond max_pages.  New slots hold whatever their pages
+ * held.  No passage: a convention of this library.
+ */
+int tq1_pages_resize(const tq1_page_pool* pool, const int32_t* seqs, const int32_t* new_len, int64_t n, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/*
+ * Fork: children[i] (distinct, empty) become copies of parents[i], i < n <=
+ * n_seqs (a parent may occur several times, but not as a child).  Full pages
+ * are shared; a partly filled last page is copied to the lowest free one, in
+ * the order of the arguments.  A child that is not empty is skipped and sets
+ * TQ1_ERR_BAD_ID; children from the first one on that there is no page for
+ * stay empty and TQ1_ERR_NO_PAGES is set.
+ * No passage: a convention of this library.
+ */
+int tq1_pages_fork(const tq1_page_pool* pool, const int32_t* parents, const int32_t* children, int64_t n, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * Compact: with L pages in use, the j-th page in use at or past L moves to
+ * the j-th free page below L, so that afterwards exactly pages 0 .. L-1 are
+ * in use; tables and counts follow.
+ * No passage: a convention of this library.
+ */
+int tq1_pages_compact(const tq1_page_pool* pool, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
