@@ -90,18 +90,6 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Store elements e .. e+3 of an output row.
-template <typename T>
-__device__ __forceinline__ void store4(const AttnArgs& a, int64_t tok, int head, int d, int e, float4 v) {
-  const int64_t at = tok * a.ldo + static_cast<int64_t>(head) * d + e;
-  if (a.out_f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
-}
-
 }  // namespace
 
 template <typename T, int D>
@@ -308,7 +296,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
           out[r] = mx;
           out[kARows + r] = lt;
         }
-        *reinterpret_cast<float4*>(out + 2 * kARows + r * D + col) = v;
+        *reinterpret_cast<float4*>(out + slot_o(kARows, r, col)) = v;
       }
     }
     if (!whole && tid == 0) {
@@ -348,16 +336,17 @@ __global__ void __launch_bounds__(256)
   int last = c + 1;
   while (last < ctas && !parts[2 * last].ends) ++last;
   const size_t sf = join_slot_floats(slot_rows, D);
+  const int lrow = (slot_rows + 3) & ~3;
   for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < p.rows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+    const int r = e % p.rows, col = (e / p.rows) * 4;
     const float* s = slots + slot * sf;
-    float m = s[r], l = s[slot_rows + r];
-    float4 v = *reinterpret_cast<const float4*>(s + 2 * slot_rows + static_cast<size_t>(r) * D + col);
+    float m = s[r], l = s[lrow + r];
+    float4 v = *reinterpret_cast<const float4*>(s + slot_o(slot_rows, r, col));
 #pragma unroll 4
     for (int k = c + 1; k <= last && k < ctas; ++k) {
       s = slots + 2 * k * sf;
-      const float mk = s[r], lk = s[slot_rows + r];
-      const float4 x = *reinterpret_cast<const float4*>(s + 2 * slot_rows + static_cast<size_t>(r) * D + col);
+      const float mk = s[r], lk = s[lrow + r];
+      const float4 x = *reinterpret_cast<const float4*>(s + slot_o(slot_rows, r, col));
       const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.0f : mn;
       const float f0 = exp2f(m - base), f1 = exp2f(mk - base);
       m = mn;
@@ -377,8 +366,34 @@ namespace {
 
 int attn_ctas() { return device_info().num_sms; }
 
+// Which kernel a call takes, by the rows (tokens x query heads of a kv head)
+// of an average sequence: kWarps for up to one 16-row tile, else the 128-row
+// kernel, with two such tiles side by side where one does not hold them.
+enum Route { kWarps, kTile, kTilePair };
+Route route(int64_t t, int64_t group, int64_t n_seqs) {
+  const int64_t rows = (t * group + n_seqs - 1) / n_seqs;
+  return rows <= kARows ? kWarps : rows <= (128 / group) * group ? kTile : kTilePair;
+}
+int route_rows(Route r, int group) { return r == kWarps ? kARows : attn_tile_rows(group, r == kTilePair); }
+
+template <typename Kernel, typename... Args>
+bool launch_pdl(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 template <typename T, int D>
-int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status, cudaStream_t s) {
+int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, int ctas, Part* parts, float* slots,
+                unsigned* status, cudaStream_t s) {
   using C = WarpCfg<D>;
   const DeviceInfo& di = device_info();
   static std::atomic<bool> configured[64];  // per device (racing threads configure twice: idempotent)
@@ -389,27 +404,29 @@ int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws,
       return TQ1_ERR_CUDA;
     configured[di.device].store(true, std::memory_order_release);
   }
-  const int ctas = attn_ctas();
+  const TilePlan plan = {kARows, kABlock, a.n_q / c.n_kv, a.causal, a.window};
+  return launch_pdl(attn_warp_kernel<T, D>, dim3(ctas), kAThreads, C::kSmem, s, c, b, a, plan, parts, slots, status)
+             ? TQ1_OK
+             : TQ1_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status,
+                 cudaStream_t s) {
+  const int ctas = attn_ctas(), group = a.n_q / c.n_kv;
   Part* parts = static_cast<Part*>(ws);
   float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + join_parts_bytes(ctas));
-  TilePlan plan = {kARows, kABlock, a.n_q / c.n_kv, a.causal, a.window};
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kAThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (!cuda_ok(cudaLaunchKernelEx(&cfg, attn_warp_kernel<T, D>, c, b, a, plan, parts, slots, status)))
-    return TQ1_ERR_CUDA;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 2);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_join_kernel<T, D>, a, kARows, plan.group, static_cast<const Part*>(parts),
-                                    static_cast<const float*>(slots), ctas))
+  int rc = TQ1_ERR_UNSUPPORTED;
+  if (r != kWarps) rc = launch_attn_tile(c, b, a, r == kTilePair, ctas, parts, slots, status, s);
+  if (rc == TQ1_ERR_UNSUPPORTED) {  // or strides that a tensor map cannot describe
+    r = kWarps;
+    rc = launch_warp<T, D>(c, b, a, ctas, parts, slots, status, s);
+  }
+  if (rc != TQ1_OK) return rc;
+  const int rows = route_rows(r, group);
+  const int share = (rows * (D / 4) + 1023) / 1024;  // four 4-column pieces a thread at most
+  return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 256, 0, s, a, rows, group, static_cast<const Part*>(parts),
+                    static_cast<const float*>(slots), ctas)
              ? TQ1_OK
              : TQ1_ERR_CUDA;
 }
@@ -418,16 +435,20 @@ int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws,
 
 size_t attn_workspace_bytes(const KvCache& c, int64_t t, int64_t n_q, int64_t n_seqs) {
   const int ctas = attn_ctas();
-  const size_t b = join_parts_bytes(ctas) + 2 * static_cast<size_t>(ctas) * join_slot_floats(kARows, c.d) * sizeof(float);
+  const int group = static_cast<int>(n_q / c.n_kv);
+  if (group < 1 || group > 128) return 0;
+  const int rows = max(kARows, route_rows(route(t, group, n_seqs), group));
+  const size_t b = join_parts_bytes(ctas) + 2 * static_cast<size_t>(ctas) * join_slot_floats(rows, c.d) * sizeof(float);
   return (b + 255) & ~size_t(255);
 }
 
 int launch_attn(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status, cudaStream_t s) {
+  const Route r = route(b.t, a.n_q / c.n_kv, b.n_seqs);
   if (c.d == 128)
-    return c.dtype == kBf16 ? launch_warp<__nv_bfloat16, 128>(c, b, a, ws, status, s)
-                            : launch_warp<__half, 128>(c, b, a, ws, status, s);
-  return c.dtype == kBf16 ? launch_warp<__nv_bfloat16, 64>(c, b, a, ws, status, s)
-                          : launch_warp<__half, 64>(c, b, a, ws, status, s);
+    return c.dtype == kBf16 ? launch_route<__nv_bfloat16, 128>(r, c, b, a, ws, status, s)
+                            : launch_route<__half, 128>(r, c, b, a, ws, status, s);
+  return c.dtype == kBf16 ? launch_route<__nv_bfloat16, 64>(r, c, b, a, ws, status, s)
+                          : launch_route<__half, 64>(r, c, b, a, ws, status, s);
 }
 
 }  // namespace tq1

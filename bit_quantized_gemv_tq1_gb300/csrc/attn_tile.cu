@@ -1,0 +1,735 @@
+// attn_tile.cu -- attention over the paged cache on the 5th-generation tensor
+// cores, for calls with many rows per kv head (prompt chunks).
+//
+// The mathematics and the division of work are attn.cu's and kv.cuh's; here a
+// tile is 128 rows (or two of them) and a block 128 keys:
+//   S = Q K^T   tcgen05.mma 128 x 128 x 16, both operands in shared memory
+//   P = exp2(scale log2e S - m), 16 bits, written over S in tensor memory
+//   O += P V    tcgen05.mma 128 x d x 16, P from tensor memory, V from shared
+//               memory as it lies in the cache (keys by elements: the operand's
+//               other major order), O in tensor memory
+//
+// Bound: the tensor pipe.  Per 128 x 128 keys it takes 8 d cycles for both
+// products (4096 multiply-adds a cycle), the exponentials 512; so two streams
+// of (S, P, O), one warp group each, take turns: while one's weights are
+// formed the tensor pipe does the other's products.
+//   PAIR:  a tile has two times 128 rows, a stream each, and both read the
+//          same keys (a chunk with more than 128 rows per kv head)
+//   else:  a tile has 128 rows; the streams take every other block and are
+//          joined at the tile's end (fewer rows: the cache's length is what is
+//          left to share out)
+// Rows are (token, query head of the group), token by token: a tile holds
+// floor(128 / group) whole tokens, so the queries of a tile are one box of q,
+// and every key is read once for the whole group.
+//
+// Rescaling: O stays relative to a reference maximum that is moved (and O
+// with it, through registers) only when a row's maximum has grown by more than
+// 2^8 over it; weights up to 2^8 lose nothing, 16-bit floats being relative.
+//
+// Roles: warps 0-3 and 4-7 the two streams' weights (a thread a row), warp 8
+// the matrix instructions, warp 9 the copies (TMA, a box per page and 64
+// elements, 128-byte swizzle).  Keys at or past a sequence's length are not
+// read at all where a whole page of them is, and otherwise their values are
+// overwritten with zeros in shared memory before the second product: a weight
+// of zero would not silence a NaN there.
+//
+// Every wait is bounded; the first that runs out sets an abort flag that
+// releases the others, and TQ1_ERR_TIMEOUT is raised.
+#include <atomic>
+
+#include "../../include/tq1.h"
+#include "kv.cuh"
+#include "tcgen05.cuh"
+#include "tq1_internal.h"
+
+namespace tq1 {
+
+namespace {
+
+constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9;  // warps 10 and 11 make the third warp group whole
+// Registers per thread: 384 x 168 at launch = 2 x 128 x 224 + 128 x 56.
+constexpr int kWeightRegs = 224, kOtherRegs = 56;
+constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
+constexpr int kTBlock = 128;  // keys of a block
+constexpr float kMoveAt = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
+
+template <int D, bool PAIR>
+struct TileCfg {
+  static constexpr uint32_t kHalf = kTBlock * 128;             // 64 elements of 128 rows
+  static constexpr uint32_t kTile = (D / 64) * kHalf;          // 128 rows of q, keys or values
+  static constexpr int kQTiles = PAIR ? 2 : 1;
+  static constexpr uint32_t kStatic = PAIR ? 1536 : 3584;      // barriers, and the streams' join
+  static constexpr int kRing = static_cast<int>((232448 - kStatic - 1024) / kTile) - kQTiles;
+  static constexpr uint32_t kSmem = (kQTiles + kRing) * kTile + 1024;
+  static constexpr int kAhead = PAIR ? 1 : 2;  // blocks of keys issued before a block's second product
+  static constexpr uint32_t kS = 0, kO = 256;  // tensor-memory columns: S of stream s at 128 s, O at kO + s D
+};
+
+struct TileKernelArgs {
+  KvCache c;
+  KvBatch b;
+  AttnArgs a;
+  TilePlan plan;
+  Part* parts;
+  float* slots;
+  unsigned* status;
+  int stream_rows, stream_tokens;  // rows and tokens of a stream: floor(128 / group) tokens
+  int box_keys;                    // keys of a copied box
+};
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  // The warp's lanes leave together, with one answer.
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+}
+
+// Keys by elements (K order down the rows, 64 elements of N along a row):
+// the operand's N-major order, 128-byte swizzle.  Blocks of 64 elements lie
+// `lead` bytes apart, groups of eight keys 1024.
+__device__ __forceinline__ uint64_t umma_desc_nmajor(uint32_t saddr, uint32_t lead) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D (TMEM) += A (shared memory) * B (shared memory).
+__device__ __forceinline__ void umma_ss(uint32_t dtmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Uses of v stay behind the wait that precedes this.
+__device__ __forceinline__ void hold(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i])::"memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (a.x * b + c, a.y * b + c)
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+  uint64_t r, x, y, z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(z) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r, x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+
+// One tile's share of this CTA, as every role sees it.
+struct Segment {
+  int head, seq, tile, blk, nb, todo;  // blocks [blk, blk + todo) of the tile's nb
+  int first_key;                       // of block blk
+  int row0, rows, tok0, hi;            // rows of the tile; first token; keys [.., hi) that some row sees
+  bool empty;                          // no row sees a key: nothing is read
+  Seq sq;
+};
+
+__device__ __forceinline__ void open_segment(const TileKernelArgs& k, Segment& g, int64_t left) {
+  int fb;
+  tile_blocks(k.plan, g.sq, g.tile, fb, g.nb);
+  g.todo = static_cast<int>(min(static_cast<int64_t>(g.nb - g.blk), left));
+  g.first_key = (fb + g.blk) * kTBlock;
+  g.row0 = g.tile * k.plan.rows;
+  g.rows = min(k.plan.rows, g.sq.n * k.plan.group - g.row0);
+  g.tok0 = g.row0 / k.plan.group;
+  const int last = (g.row0 + g.rows - 1) / k.plan.group, before = g.sq.len - g.sq.n;
+  g.hi = k.plan.causal ? min(g.sq.len, before + last + 1) : g.sq.len;
+  g.empty = g.hi <= (k.plan.window ? max(0, before + g.tok0 - k.plan.window + 1) : 0);
+}
+
+}  // namespace
+
+template <typename T, int D, bool PAIR>
+__global__ void __launch_bounds__(kTThreads, 1)
+    attn_tile_kernel(const TileKernelArgs k, const __grid_constant__ CUtensorMap tmq,
+                     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using C = TileCfg<D, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing];
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], swap;
+  __shared__ float s_ml[2][2][kTRows];  // [stream][m, l][row]: the streams' join
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int* abort_flag = &s_abort;
+  const uint32_t raw = smem_addr(smem_raw), sbase = (raw + 1023u) & ~1023u;
+  uint8_t* const sm = smem_raw + (sbase - raw);
+  const uint32_t q_at = sbase, ring_at = sbase + C::kQTiles * C::kTile;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmq)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmv)) : "memory");
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], kTRows);
+      mbar_init(&o_full[s], 1);
+    }
+    mbar_init(&swap, 2 * kTRows);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Start st = find_start<kTThreads>(k.plan, k.b, k.c.n_kv, cta, ctas, reinterpret_cast<int*>(sm));
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies below write where the search wrote
+  __syncthreads();
+  if (tid < 2) k.parts[2 * cta + tid].rows = 0;
+  __syncthreads();
+  Segment g;
+  g.head = st.head;
+  g.seq = st.seq;
+  g.tile = st.tile;
+  g.blk = st.block;
+  int64_t left = st.units;
+  if (left > 0) g.sq = load_seq(k.b, g.seq);
+  auto advance = [&]() {
+    left -= g.todo;
+    if (left > 0) {
+      next_tile(k.plan, k.b, g.head, g.seq, g.tile, g.sq);
+      g.blk = 0;
+    }
+  };
+
+  if (warp < kMmaWarp) {
+    // ---------------------------------------------------------- weights --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
+    const int s = warp >> 2, row = tid & (kTRows - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t st_at = tmem + lanes + C::kS + 128 * s, o_at = tmem + lanes + C::kO + s * D;
+    const float sc = k.a.scale * kLog2e;
+    uint32_t done = 0;   // blocks this stream has done, over all segments
+    uint32_t swaps = 0;  // phases of `swap` passed
+    bool ok = true;
+    for (bool first_seg = true; left > 0 && ok; first_seg = false) {
+      open_segment(k, g, left);
+      // This thread's row: its place in the tile, its keys [lo, hi).  Lanes
+      // past the stream's rows (or the sequence's) compute on what lies in
+      // shared memory and store nothing.
+      const int trow = PAIR ? s * k.stream_rows + row : row;
+      const bool there = row < k.stream_rows && trow < g.rows;
+      const int tok = (g.row0 + trow) / k.plan.group, qh = g.head * k.plan.group + (g.row0 + trow) - tok * k.plan.group;
+      int lo = 0, hi = 0x7fffffff;
+      if (there) {
+        const int pos = g.sq.len - g.sq.n + tok;
+        hi = k.plan.causal ? min(g.sq.len, pos + 1) : g.sq.len;
+        lo = k.plan.window ? max(0, pos - k.plan.window + 1) : 0;
+      }
+      float m = -INFINITY, l = 0.0f;  // the row's reference maximum (of S) and its sum
+      if (!g.empty) {
+        for (int i = PAIR ? 0 : s; i < g.todo; i += PAIR ? 1 : 2) {
+          const int key0 = g.first_key + i * kTBlock;
+          if (!wait_all(&s_full[s], done & 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld<32>(st_at + 32 * c, v[c]);
+          wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) hold(v[c]);
+          if (__any_sync(0xffffffffu, lo > key0 || hi < key0 + kTBlock)) {
+            const int a = lo - key0, b = hi - key0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * c + j < a || 32 * c + j >= b) v[c][j] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+#pragma unroll
+            for (int j = 2; j < 32; j += 2)
+              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(v[c][j])), __uint_as_float(v[c][j + 1]));
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool opening = i < 2 && (!PAIR || i == 0);  // nothing in O yet
+          if (opening) {
+            m = mt;
+          } else {
+            const bool move = mt > m && (mt - m) * sc > kMoveAt;
+            if (__any_sync(0xffffffffu, move)) {
+              float keep = 1.0f;
+              if (move) {
+                keep = exp2_fast((m - mt) * sc);
+                m = mt;
+                l *= keep;
+              }
+              // O is at rest once the block before has been added to it.
+              if (!wait_all(&o_full[s], (done - 1) & 1u, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld<32>(o_at + 32 * c, o);
+                wait_ld();
+                hold(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                tmem_st32(o_at + 32 * c, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.0f : -m * sc;  // no key seen yet: all weights are exp2(-inf) = 0
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // The weights enter the second product as 16-bit numbers of V's
+            // type (the instruction wants one type); their sum stays fp32.
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int c = 2 * h + (j >> 4), e = 2 * (j & 15);
+              float2 x = fma2(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc, base);
+              x.x = exp2_fast(x.x);
+              x.y = exp2_fast(x.y);
+              sum[j & 1] = add2(sum[j & 1], x);
+              p[j] = pack2<T>(x.x, x.y);
+            }
+            tmem_st32(st_at + 32 * h, p);
+          }
+          const float2 both = add2(sum[0], sum[1]);
+          l += both.x + both.y;
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          tc_fence_before();
+          mbar_arrive(&p_full[s]);
+          ++done;
+        }
+        if (!ok) break;
+      }
+      const bool mine = !g.empty && (PAIR || s < g.todo);  // this stream's O holds something
+      if (mine) {
+        if (!wait_all(&o_full[s], (done - 1) & 1u, abort_flag)) break;
+        tc_fence_after();
+      }
+      // Out: the row over its sum, or, of a tile that others share, the row
+      // as it is.  Two streams on one tile first tell each other their m and
+      // l; then each does half the columns of both.
+      float mrow = m == -INFINITY ? m : m * sc, lrow = l, f0 = 1.0f, f1 = 0.0f;
+      if (!PAIR) {
+        s_ml[s][0][row] = mrow;
+        s_ml[s][1][row] = l;
+        tc_fence_before();
+        mbar_arrive(&swap);
+        if (!wait_all(&swap, swaps & 1u, abort_flag)) break;
+        ++swaps;
+        tc_fence_after();
+        const float m0 = s_ml[0][0][row], m1 = s_ml[1][0][row];
+        mrow = fmaxf(m0, m1);
+        f0 = m0 == -INFINITY ? 0.0f : exp2f(m0 - mrow);
+        f1 = m1 == -INFINITY ? 0.0f : exp2f(m1 - mrow);
+        lrow = f0 * s_ml[0][1][row] + f1 * s_ml[1][1][row];
+      }
+      const bool whole = g.blk == 0 && g.todo == g.nb;
+      const int slot = first_seg ? 2 * cta : 2 * cta + 1;
+      float* out = k.slots + slot * join_slot_floats(k.plan.rows, D);
+      const float inv = lrow > 0.0f ? 1.0f / lrow : (lrow == 0.0f ? 0.0f : lrow);  // a row that sees nothing is zero
+      const int64_t at = static_cast<int64_t>(g.sq.q0 + tok) * k.a.ldo + static_cast<int64_t>(qh) * D;
+      constexpr int kCols = PAIR ? D : D / 2;
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) {
+        const int col = (PAIR ? 0 : s * kCols) + 32 * c;
+        float x[32];
+        if (g.empty) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+        } else {
+          uint32_t o[32];
+          tmem_ld<32>(tmem + lanes + C::kO + (PAIR ? s * D : 0) + col, o);
+          wait_ld();
+          hold(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = f0 == 0.0f ? 0.0f : f0 * __uint_as_float(o[j]);
+          if (!PAIR && g.todo > 1) {
+            tmem_ld<32>(tmem + lanes + C::kO + D + col, o);
+            wait_ld();
+            hold(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] += f1 == 0.0f ? 0.0f : f1 * __uint_as_float(o[j]);
+          }
+        }
+        if (!there) continue;
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(out + slot_o(k.plan.rows, trow, col + j)) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        } else if (k.a.out_f32) {
+          float4* dst = reinterpret_cast<float4*>(static_cast<float*>(k.a.out) + at + col);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j] = make_float4(x[4 * j] * inv, x[4 * j + 1] * inv, x[4 * j + 2] * inv, x[4 * j + 3] * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(k.a.out) + at + col);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_uint4(pack2<T>(x[8 * j] * inv, x[8 * j + 1] * inv), pack2<T>(x[8 * j + 2] * inv, x[8 * j + 3] * inv),
+                                pack2<T>(x[8 * j + 4] * inv, x[8 * j + 5] * inv), pack2<T>(x[8 * j + 6] * inv, x[8 * j + 7] * inv));
+        }
+      }
+      if (!whole) {
+        if (there && (PAIR || s == 0)) {
+          out[trow] = mrow;
+          out[((k.plan.rows + 3) & ~3) + trow] = lrow;
+        }
+        if (tid == 0) {
+          Part& p = k.parts[slot];
+          p.head = g.head;
+          p.q0 = g.sq.q0;
+          p.row0 = g.row0;
+          p.starts = g.blk == 0;
+          p.ends = g.blk + g.todo == g.nb;
+          p.rows = g.rows;
+        }
+      }
+      if (!PAIR) {
+        // The other stream has read this one's O and s_ml before either goes on.
+        tc_fence_before();
+        mbar_arrive(&swap);
+        if (!wait_all(&swap, swaps & 1u, abort_flag)) break;
+        ++swaps;
+        tc_fence_after();
+      }
+      advance();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
+      // ------------------------------------------------------------- MMA --
+      // All lanes walk the loop (they zero values past a sequence's end
+      // together); lane 0 waits and issues.
+      constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
+      constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
+      uint32_t ri = 0, rph = 0;        // ring slot to be consumed next, its phase
+      uint32_t pdone[2] = {0, 0};      // blocks of weights taken from each stream
+      uint32_t segs = 0;
+      bool ok = true;
+      uint64_t* last_bar = nullptr;    // the latest commit, for a clean end after an abort
+      uint32_t last_ph = 0;
+      auto take = [&](uint64_t* bar, uint32_t ph) {
+        int r = 1;
+        if (lane == 0) r = spin_wait_or_abort(bar, ph, abort_flag) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+        return ok;
+      };
+      auto step = [&]() {
+        if (++ri == C::kRing) {
+          ri = 0;
+          rph ^= 1u;
+        }
+      };
+      auto product_s = [&](int s, uint32_t slot) {
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t qd = umma_desc_sw128(q_at + (PAIR ? s : 0) * C::kTile), kd = umma_desc_sw128(ring_at + slot * C::kTile);
+  #pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
+            umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[s]);
+        }
+      };
+      auto product_o = [&](int s, uint32_t slot, int steps, bool accumulate) {
+        if (lane == 0) {
+          tc_fence_after();
+          const uint64_t vd = umma_desc_nmajor(ring_at + slot * C::kTile, C::kHalf);
+          for (int ks = 0; ks < steps; ++ks)
+            umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
+                    accumulate || ks > 0 ? 1u : 0u);
+          umma_commit(&o_full[s]);
+        }
+      };
+      auto release = [&](uint32_t slot, uint32_t ph) {
+        if (lane == 0) umma_commit(&empty[slot]);
+        last_bar = &empty[slot];
+        last_ph = ph;
+      };
+      // Zeros over the values of slot from key `from` of the block to the end
+      // of its group of 16.
+      auto silence = [&](uint32_t slot, int from) {
+        const int upto = (from + 15) & ~15;
+        for (int r = from; r < upto; ++r)
+          for (int c = lane; c < (D / 64) * 8; c += 32)
+            *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      };
+      while (left > 0 && ok) {
+        open_segment(k, g, left);
+        if (!g.empty) {
+          if (!take(&q_full, segs & 1u)) break;
+          const int n = g.todo;
+          int keys_issued = 0;
+          // Blocks of keys ahead of the first weights.
+          for (; keys_issued < C::kAhead && keys_issued < n; ++keys_issued) {
+            if (!take(&full[ri], rph)) break;
+            product_s(PAIR ? 0 : keys_issued, ri);
+            if (PAIR) product_s(1, ri);
+            release(ri, rph);
+            step();
+          }
+          if (!ok) break;
+          for (int i = 0; i < n && ok; ++i) {
+            const int key0 = g.first_key + i * kTBlock;
+            const int seen = min(kTBlock, g.hi - key0), steps = (seen + 15) >> 4, have = g.sq.len - key0;
+            const uint32_t vs = ri, vph = rph;
+            step();
+            const bool more = i + C::kAhead < n;
+            const uint32_t ks = ri, kph = rph;
+            if (more) step();
+  #pragma unroll
+            for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
+              const int s = PAIR ? u : (i & 1);
+              if (!take(&p_full[s], pdone[s] & 1u)) break;
+              ++pdone[s];
+              if (u == 0) {
+                if (!take(&full[vs], vph)) break;
+                if (have < 16 * steps) silence(vs, have);
+              }
+              product_o(s, vs, steps, PAIR ? i > 0 : i > 1);
+              if (u == (PAIR ? 1 : 0)) release(vs, vph);
+              if (more) {
+                if (u == 0 && !take(&full[ks], kph)) break;
+                product_s(s, ks);
+                if (u == (PAIR ? 1 : 0)) release(ks, kph);
+              }
+            }
+          }
+          if (!ok) break;
+          if (lane == 0) umma_commit(&q_empty);
+          ++segs;
+        }
+        advance();
+      }
+      // After an abort, let the products already issued finish (bounded).
+      if (lane == 0 && *abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
+    } else if (warp == kLoadWarp) {
+      // ----------------------------------------------------------- copies --
+      uint32_t ri = 0, rph = 0, segs = 0;
+      bool ok = true;
+      uint64_t* last_bar = nullptr;
+      uint32_t last_ph = 0;
+      const int boxes = kTBlock / k.box_keys;  // of a block
+      const int half = lane & (D / 64 - 1), box = lane / (D / 64);
+      auto take = [&](uint64_t* bar, uint32_t ph) {
+        int r = 1;
+        if (lane == 0) r = wait_or_abort(bar, ph, abort_flag) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, r, 0) != 0;
+        return ok;
+      };
+      // The page of this lane's box of the block from key0 on: -1 (read as
+      // zeros) where the table names none, -2 past the sequence's end.
+      auto page_of = [&](int key0) {
+        const int key = key0 + box * k.box_keys;
+        if (box >= boxes || key >= g.sq.len) return -2;
+        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
+        if (id >= 0 && id < k.c.n_pages) return id;
+        raise_status(k.status, kStatusBadId);
+        return -1;
+      };
+      auto copy = [&](const CUtensorMap* map, int key0, int page) {
+        if (!take(&empty[ri], rph ^ 1u)) return false;
+        const uint32_t live = __ballot_sync(0xffffffffu, page != -2);
+        if (lane == 0) mbar_arrive_expect_tx(&full[ri], __popc(live) * k.box_keys * 128);
+        __syncwarp();
+        if (page != -2)
+          tma_load_4d(ring_at + ri * C::kTile + half * C::kHalf + box * k.box_keys * 128, map, 64 * half,
+                      (key0 + box * k.box_keys) & (k.c.page_size - 1), g.head, page, &full[ri]);
+        last_bar = &full[ri];
+        last_ph = rph;
+        if (++ri == C::kRing) {
+          ri = 0;
+          rph ^= 1u;
+        }
+        return true;
+      };
+      while (left > 0 && ok) {
+        open_segment(k, g, left);
+        if (!g.empty) {
+          int page[C::kAhead];
+  #pragma unroll
+          for (int i = 0; i < C::kAhead; ++i) page[i] = i < g.todo ? page_of(g.first_key + i * kTBlock) : -2;
+          if (!take(&q_empty, (segs & 1u) ^ 1u)) break;
+          if (lane == 0) mbar_arrive_expect_tx(&q_full, C::kQTiles * (D / 64) * k.stream_rows * 128);
+          __syncwarp();
+          if (lane < C::kQTiles * (D / 64)) {
+            const int qs = lane / (D / 64), qhalf = lane & (D / 64 - 1);
+            tma_load_3d(q_at + qs * C::kTile + qhalf * C::kHalf, &tmq, 64 * qhalf, g.head * k.plan.group,
+                        g.sq.q0 + g.tok0 + qs * k.stream_tokens, &q_full);
+          }
+          ++segs;
+          for (int i = 0; i < C::kAhead && i < g.todo && ok; ++i) copy(&tmk, g.first_key + i * kTBlock, page[i]);
+          for (int i = 0; i < g.todo && ok; ++i) {
+            const int next = i + C::kAhead, key = g.first_key + i * kTBlock;
+            const int np = next < g.todo ? page_of(g.first_key + next * kTBlock) : -2;
+            if (!copy(&tmv, key, page[0])) break;
+            if (next < g.todo && !copy(&tmk, g.first_key + next * kTBlock, np)) break;
+  #pragma unroll
+            for (int j = 0; j + 1 < C::kAhead; ++j) page[j] = page[j + 1];
+            page[C::kAhead - 1] = np;
+          }
+          if (!ok) break;
+        }
+        advance();
+      }
+      // Copies still in flight must land before the CTA leaves.
+      if (lane == 0 && *abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && *abort_flag) raise_status(k.status, kStatusTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+namespace {
+
+bool make_tensor_map(CUtensorMap* map, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                     const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D, bool PAIR>
+int launch_cfg(const TileKernelArgs& k, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv, int ctas,
+               cudaStream_t s) {
+  using C = TileCfg<D, PAIR>;
+  const DeviceInfo& di = device_info();
+  static std::atomic<bool> configured[64];  // per device (racing threads configure twice: idempotent)
+  if (di.device < 0 || di.device >= 64) return TQ1_ERR_CUDA;
+  if (C::kSmem + C::kStatic > di.max_smem_optin) return TQ1_ERR_UNSUPPORTED;
+  if (!configured[di.device].load(std::memory_order_acquire)) {
+    if (!cuda_ok(cudaFuncSetAttribute(attn_tile_kernel<T, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(C::kSmem))))
+      return TQ1_ERR_CUDA;
+    configured[di.device].store(true, std::memory_order_release);
+  }
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, attn_tile_kernel<T, D, PAIR>, k, tmq, tmk, tmv)) ? TQ1_OK : TQ1_ERR_CUDA;
+}
+
+}  // namespace
+
+int attn_tile_rows(int group, bool pair) { return (kTRows / group) * group * (pair ? 2 : 1); }
+
+int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool pair, int ctas, Part* parts,
+                     float* slots, unsigned* status, cudaStream_t s) {
+  const int group = a.n_q / c.n_kv, tokens = kTRows / group;
+  TileKernelArgs k = {};
+  k.c = c;
+  k.b = b;
+  k.a = a;
+  k.plan = {attn_tile_rows(group, pair), kTBlock, group, a.causal, a.window};
+  k.parts = parts;
+  k.slots = slots;
+  k.status = status;
+  k.stream_rows = tokens * group;
+  k.stream_tokens = tokens;
+  k.box_keys = c.page_size < kTBlock ? c.page_size : kTBlock;
+  CUtensorMap tmq, tmk, tmv;
+  {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(a.n_q), static_cast<cuuint64_t>(b.t)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.d) * 2, static_cast<cuuint64_t>(a.ldq) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
+    if (!make_tensor_map(&tmq, c.dtype, 3, a.q, dims, strides, box)) return TQ1_ERR_UNSUPPORTED;
+  }
+  {
+    // A dimension of one element is never stepped along; its stride may then
+    // be anything in the caller's hands and is replaced by a valid one.
+    const int64_t row = c.slot_stride * 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.n_kv), static_cast<cuuint64_t>(c.n_pages > 0 ? c.n_pages : 1)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(c.n_kv > 1 ? c.head_stride * 2 : row),
+                                   static_cast<cuuint64_t>(c.n_pages > 1 ? c.page_stride * 2 : row)};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(k.box_keys), 1, 1};
+    if (!make_tensor_map(&tmk, c.dtype, 4, c.k, dims, strides, box)) return TQ1_ERR_UNSUPPORTED;
+    if (!make_tensor_map(&tmv, c.dtype, 4, c.v, dims, strides, box)) return TQ1_ERR_UNSUPPORTED;
+  }
+#define TQ1_TILE(T, D) (pair ? launch_cfg<T, D, true>(k, tmq, tmk, tmv, ctas, s) : launch_cfg<T, D, false>(k, tmq, tmk, tmv, ctas, s))
+  if (c.d == 128) return c.dtype == kBf16 ? TQ1_TILE(__nv_bfloat16, 128) : TQ1_TILE(__half, 128);
+  return c.dtype == kBf16 ? TQ1_TILE(__nv_bfloat16, 64) : TQ1_TILE(__half, 64);
+#undef TQ1_TILE
+}
+
+}  // namespace tq1

@@ -149,7 +149,7 @@ int tq1_rope_append(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const 
 
 size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64_t n_q, int64_t n_seqs) {
   KvCache c;
-  if (get_cache(cache, &c) != TQ1_OK || t < 0 || n_q <= 0 || n_seqs <= 0) return 0;
+  if (get_cache(cache, &c) != TQ1_OK || t < 0 || n_q <= 0 || n_q > 65536 || n_seqs <= 0 || t > (int64_t{1} << 24)) return 0;
   if (!status_word()) return 0;
   return attn_workspace_bytes(c, t, n_q, n_seqs);
 }

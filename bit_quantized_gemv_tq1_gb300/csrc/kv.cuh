@@ -241,8 +241,23 @@ struct Part {
 };
 
 // Workspace of `ctas` CTAs: their parts, then two slots each of rows * (d + 2)
-// floats: m [rows], l [rows], O [rows][d].
+// floats: m [rows] (in log2 units), l [rows], then O four columns at a time,
+// [d/4][rows][4], so that threads of consecutive rows store consecutive
+// 16-byte pieces.
 inline __host__ __device__ size_t join_parts_bytes(int ctas) { return static_cast<size_t>(ctas) * 2 * sizeof(Part); }
-inline __host__ __device__ size_t join_slot_floats(int rows, int d) { return static_cast<size_t>(rows) * (d + 2); }
+inline __host__ __device__ size_t join_slot_floats(int rows, int d) { return static_cast<size_t>((rows + 3) & ~3) * (d + 2); }
+__device__ __forceinline__ int slot_o(int rows, int r, int col) { return 2 * ((rows + 3) & ~3) + col * rows + 4 * r; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Store elements e .. e+3 of an output row.
+template <typename T>
+__device__ __forceinline__ void store4(const AttnArgs& a, int64_t tok, int head, int d, int e, float4 v) {
+  const int64_t at = tok * a.ldo + static_cast<int64_t>(head) * d + e;
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack2<T>(v.x, v.y), pack2<T>(v.z, v.w));
+}
 
 }  // namespace tq1

@@ -53,6 +53,15 @@ struct AttnArgs {
   int n_q, causal, window, out_f32;
 };
 
+struct Part;  // kv.cuh
+
+// The 128-row tensor-core kernel (`pair`: two such tiles side by side).
+// Returns TQ1_ERR_UNSUPPORTED, launching nothing, for strides that a tensor
+// map cannot describe.
+int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool pair, int ctas, Part* parts,
+                     float* slots, unsigned* status, cudaStream_t s);
+int attn_tile_rows(int group, bool pair);
+
 size_t attn_workspace_bytes(const KvCache& c, int64_t t, int64_t n_q, int64_t n_seqs);
 int launch_attn(const KvCache& c, const KvBatch& b, const AttnArgs& a, void* ws, unsigned* status, cudaStream_t s);
 
