@@ -29,8 +29,8 @@
 // Roles: warps 0-3 and 4-7 the two streams' weights (a thread a row), warp 8
 // the matrix instructions, warp 9 the copies (TMA, a box per page and 64
 // elements, 128-byte swizzle).  Keys at or past a sequence's length are not
-// read at all where a whole page of them is, and otherwise their values are
-// overwritten with zeros in shared memory before the second product: a weight
+// read at all where a whole page of them is, and otherwise warp 10 overwrites
+// their values with zeros in shared memory before the second product: a weight
 // of zero would not silence a NaN there.
 //
 // Every wait is bounded; the first that runs out sets an abort flag that
@@ -46,9 +46,9 @@ namespace tq1 {
 
 namespace {
 
-constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9;  // warps 10 and 11 make the third warp group whole
-// Registers per thread: 384 x 168 at launch = 2 x 128 x 224 + 128 x 56.
-constexpr int kWeightRegs = 224, kOtherRegs = 56;
+constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;  // warp 11 makes the third warp group whole
+// Registers per thread: 384 x 168 at launch = 2 x 128 x 208 + 128 x 88.
+constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
 constexpr int kTBlock = 128;  // keys of a block
 constexpr float kMoveAt = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
@@ -78,8 +78,10 @@ struct TileKernelArgs {
 };
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  // The warp's lanes leave together, with one answer.
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag));
+  bool there = false;
+  for (int i = 0; i < 64 && !there; ++i) there = mbar_try_wait(bar, parity);
+  if (!there) there = wait_or_abort(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, there);  // the warp's lanes leave together, with one answer
 }
 
 // Keys by elements (K order down the rows, 64 elements of N along a row):
@@ -124,7 +126,7 @@ __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.
 // Uses of v stay behind the wait that precedes this.
 __device__ __forceinline__ void hold(uint32_t (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i])::"memory");
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                      const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using C = TileCfg<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing];
+  __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing], tail[C::kRing];
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], swap;
   __shared__ float s_ml[2][2][kTRows];  // [stream][m, l][row]: the streams' join
   __shared__ uint32_t s_tmem;
@@ -202,6 +204,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&tail[i], 1);
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -283,13 +286,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
           wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) hold(v[c]);
-          if (__any_sync(0xffffffffu, lo > key0 || hi < key0 + kTBlock)) {
-            const int a = lo - key0, b = hi - key0;
+          if (__any_sync(0xffffffffu, lo > key0 || hi - kTBlock < key0)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) {
+              const int a = min(max(lo - key0 - 32 * c, 0), 32), b = min(max(hi - key0 - 32 * c, 0), 32);
+              const uint32_t seen = (b == 32 ? ~0u : (1u << b) - 1u) & (a == 32 ? 0u : ~0u << a);
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (32 * c + j < a || 32 * c + j >= b) v[c][j] = 0xff800000u;
+                if (!(seen & (1u << j))) v[c][j] = 0xff800000u;
+            }
           }
           float mx[4];
 #pragma unroll
@@ -454,117 +459,141 @@ __global__ void __launch_bounds__(kTThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
-      // ------------------------------------------------------------- MMA --
-      // All lanes walk the loop (they zero values past a sequence's end
-      // together); lane 0 waits and issues.
-      constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      // ----------------------------------------------------------- MMA --
+      // One thread.  In a step (a block's second product and the first
+      // product kAhead blocks on) it takes the streams in turn.
+      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
       constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
-      uint32_t ri = 0, rph = 0;        // ring slot to be consumed next, its phase
-      uint32_t pdone[2] = {0, 0};      // blocks of weights taken from each stream
-      uint32_t segs = 0;
-      bool ok = true;
-      uint64_t* last_bar = nullptr;    // the latest commit, for a clean end after an abort
-      uint32_t last_ph = 0;
-      auto take = [&](uint64_t* bar, uint32_t ph) {
-        int r = 1;
-        if (lane == 0) r = spin_wait_or_abort(bar, ph, abort_flag) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, r, 0) != 0;
-        return ok;
-      };
-      auto step = [&]() {
-        if (++ri == C::kRing) {
-          ri = 0;
-          rph ^= 1u;
-        }
-      };
-      auto product_s = [&](int s, uint32_t slot) {
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t qd = umma_desc_sw128(q_at + (PAIR ? s : 0) * C::kTile), kd = umma_desc_sw128(ring_at + slot * C::kTile);
-  #pragma unroll
+      if (lane == 0) {
+        uint32_t ri = 0, rph = 0;      // ring slot to be consumed next, its phase
+        uint32_t pph[2] = {0, 0};      // phases of p_full
+        uint32_t qph = 0, tph = 0;     // of q_full, and of each slot's tail (a bit per slot)
+        bool ok = true;
+        uint64_t* last_bar = nullptr;  // the latest release of a slot, for a clean end after an abort
+        uint32_t last_ph = 0;
+        const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
+        const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
+        auto step = [&]() {
+          if (++ri == C::kRing) {
+            ri = 0;
+            rph ^= 1u;
+          }
+        };
+        auto product_s = [&](int s, uint32_t slot) {
+          const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
+#pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
             umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
           }
           umma_commit(&s_full[s]);
-        }
-      };
-      auto product_o = [&](int s, uint32_t slot, int steps, bool accumulate) {
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t vd = umma_desc_nmajor(ring_at + slot * C::kTile, C::kHalf);
-          for (int ks = 0; ks < steps; ++ks)
-            umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
-                    accumulate || ks > 0 ? 1u : 0u);
+        };
+        auto product_o = [&](int s, uint32_t slot, int steps, uint32_t accumulate) {
+          const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kTBlock / 16; ++ks)
+            if (ks < steps)
+              umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
+                      ks > 0 ? 1u : accumulate);
           umma_commit(&o_full[s]);
+        };
+        auto release = [&](uint32_t slot, uint32_t ph) {
+          umma_commit(&empty[slot]);
+          last_bar = &empty[slot];
+          last_ph = ph;
+        };
+        while (left > 0 && ok) {
+          open_segment(k, g, left);
+          if (!g.empty) {
+            const int n = g.todo;
+            ok = spin_wait_or_abort(&q_full, qph, abort_flag);
+            qph ^= 1u;
+            for (int i = 0; ok && i < C::kAhead && i < n; ++i) {
+              ok = spin_wait_or_abort(&full[ri], rph, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              product_s(PAIR ? 0 : i, ri);
+              if (PAIR) product_s(1, ri);
+              release(ri, rph);
+              step();
+            }
+            for (int i = 0; ok && i < n; ++i) {
+              const int key0 = g.first_key + i * kTBlock;
+              const int steps = (min(kTBlock, g.hi - key0) + 15) >> 4;
+              const bool cut = g.sq.len - key0 < 16 * steps;  // the tail warp has zeroed what lies past the end
+              const uint32_t vs = ri, vph = rph;
+              step();
+              const bool more = i + C::kAhead < n;
+              const uint32_t ks = ri, kph = rph;
+              if (more) step();
+#pragma unroll
+              for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
+                const int s = PAIR ? u : (i & 1);
+                if (u == 0) {
+                  ok = cut ? spin_wait_or_abort(&tail[vs], (tph >> vs) & 1u, abort_flag)
+                           : spin_wait_or_abort(&full[vs], vph, abort_flag);
+                  if (!ok) break;
+                  if (cut) tph ^= 1u << vs;
+                }
+                ok = spin_wait_or_abort(&p_full[s], (PAIR ? pph[u] : s ? pph[1] : pph[0]), abort_flag);
+                if (!ok) break;
+                if (PAIR)
+                  pph[u] ^= 1u;
+                else if (s)
+                  pph[1] ^= 1u;
+                else
+                  pph[0] ^= 1u;
+                tc_fence_after();
+                product_o(s, vs, steps, (PAIR ? i > 0 : i > 1) ? 1u : 0u);
+                if (u == (PAIR ? 1 : 0)) release(vs, vph);
+                if (more) {
+                  if (u == 0) {
+                    ok = spin_wait_or_abort(&full[ks], kph, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                  }
+                  product_s(s, ks);
+                  if (u == (PAIR ? 1 : 0)) release(ks, kph);
+                }
+              }
+            }
+            if (!ok) break;
+            umma_commit(&q_empty);
+          }
+          advance();
         }
-      };
-      auto release = [&](uint32_t slot, uint32_t ph) {
-        if (lane == 0) umma_commit(&empty[slot]);
-        last_bar = &empty[slot];
-        last_ph = ph;
-      };
-      // Zeros over the values of slot from key `from` of the block to the end
-      // of its group of 16.
-      auto silence = [&](uint32_t slot, int from) {
-        const int upto = (from + 15) & ~15;
-        for (int r = from; r < upto; ++r)
-          for (int c = lane; c < (D / 64) * 8; c += 32)
-            *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      };
+        // After an abort, let the products already issued finish (bounded).
+        if (*abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
+      }
+    } else if (warp == kTailWarp) {
+      // ---------------------------------------------------------- tails --
+      // Zeros over the values past a sequence's end, up to the end of the
+      // last group of 16 that is multiplied.  The last values of a segment
+      // are its last ring slot.  A barrier per slot: the slot is not filled
+      // again before its products are done, so no phase can be missed.
+      uint32_t slots_done = 0;
+      bool ok = true;
       while (left > 0 && ok) {
         open_segment(k, g, left);
         if (!g.empty) {
-          if (!take(&q_full, segs & 1u)) break;
-          const int n = g.todo;
-          int keys_issued = 0;
-          // Blocks of keys ahead of the first weights.
-          for (; keys_issued < C::kAhead && keys_issued < n; ++keys_issued) {
-            if (!take(&full[ri], rph)) break;
-            product_s(PAIR ? 0 : keys_issued, ri);
-            if (PAIR) product_s(1, ri);
-            release(ri, rph);
-            step();
+          const uint32_t at = slots_done + 2 * g.todo - 1, slot = at % C::kRing, ph = (at / C::kRing) & 1u;
+          slots_done += 2 * g.todo;
+          const int key0 = g.first_key + (g.todo - 1) * kTBlock;
+          const int upto = (min(kTBlock, g.hi - key0) + 15) & ~15, from = g.sq.len - key0;
+          if (from < upto) {
+            if (!(ok = wait_all(&full[slot], ph, abort_flag))) break;
+            for (int r = from; r < upto; ++r)
+              for (int c = lane; c < (D / 64) * 8; c += 32)
+                *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 +
+                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail[slot]);
           }
-          if (!ok) break;
-          for (int i = 0; i < n && ok; ++i) {
-            const int key0 = g.first_key + i * kTBlock;
-            const int seen = min(kTBlock, g.hi - key0), steps = (seen + 15) >> 4, have = g.sq.len - key0;
-            const uint32_t vs = ri, vph = rph;
-            step();
-            const bool more = i + C::kAhead < n;
-            const uint32_t ks = ri, kph = rph;
-            if (more) step();
-  #pragma unroll
-            for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
-              const int s = PAIR ? u : (i & 1);
-              if (!take(&p_full[s], pdone[s] & 1u)) break;
-              ++pdone[s];
-              if (u == 0) {
-                if (!take(&full[vs], vph)) break;
-                if (have < 16 * steps) silence(vs, have);
-              }
-              product_o(s, vs, steps, PAIR ? i > 0 : i > 1);
-              if (u == (PAIR ? 1 : 0)) release(vs, vph);
-              if (more) {
-                if (u == 0 && !take(&full[ks], kph)) break;
-                product_s(s, ks);
-                if (u == (PAIR ? 1 : 0)) release(ks, kph);
-              }
-            }
-          }
-          if (!ok) break;
-          if (lane == 0) umma_commit(&q_empty);
-          ++segs;
         }
         advance();
       }
-      // After an abort, let the products already issued finish (bounded).
-      if (lane == 0 && *abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
     } else if (warp == kLoadWarp) {
       // ----------------------------------------------------------- copies --
       uint32_t ri = 0, rph = 0, segs = 0;
