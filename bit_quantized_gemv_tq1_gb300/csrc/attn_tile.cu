@@ -84,6 +84,12 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, there);  // the warp's lanes leave together, with one answer
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Keys by elements (K order down the rows, 64 elements of N along a row):
 // the operand's N-major order, 128-byte swizzle.  Blocks of 64 elements lie
 // `lead` bytes apart, groups of eight keys 1024.
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = 0;  // all 512 columns were asked for: they begin at column 0
   pdl_wait();
   pdl_launch_dependents();
   const Start st = find_start<kTThreads>(k.plan, k.b, k.c.n_kv, cta, ctas, reinterpret_cast<int*>(sm));
@@ -460,12 +466,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA --
-      // One thread.  In a step (a block's second product and the first
-      // product kAhead blocks on) it takes the streams in turn.
+      // In a step (a block's second product and the first product kAhead
+      // blocks on) the streams take turns.  The whole warp walks the loop and
+      // one lane issues: what the instructions take (descriptors, addresses)
+      // is then the same in all lanes to the compiler too, which keeps it in
+      // uniform registers instead of moving it there before each of them.
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
       constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
-      if (lane == 0) {
+      const bool lead = elect_one();
+      {
         uint32_t ri = 0, rph = 0;      // ring slot to be consumed next, its phase
         uint32_t pph[2] = {0, 0};      // phases of p_full
         uint32_t qph = 0, tph = 0;     // of q_full, and of each slot's tail (a bit per slot)
@@ -482,24 +492,31 @@ __global__ void __launch_bounds__(kTThreads, 1)
         };
         auto product_s = [&](int s, uint32_t slot) {
           const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
+          if (lead) {
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
-            umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
+              umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+            }
+            umma_commit(&s_full[s]);
           }
-          umma_commit(&s_full[s]);
+          __syncwarp();
         };
         auto product_o = [&](int s, uint32_t slot, int steps, uint32_t accumulate) {
           const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
+          if (lead) {
 #pragma unroll
-          for (int ks = 0; ks < kTBlock / 16; ++ks)
-            if (ks < steps)
-              umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
-                      ks > 0 ? 1u : accumulate);
-          umma_commit(&o_full[s]);
+            for (int ks = 0; ks < kTBlock / 16; ++ks)
+              if (ks < steps)
+                umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
+                        ks > 0 ? 1u : accumulate);
+            umma_commit(&o_full[s]);
+          }
+          __syncwarp();
         };
         auto release = [&](uint32_t slot, uint32_t ph) {
-          umma_commit(&empty[slot]);
+          if (lead) umma_commit(&empty[slot]);
+          __syncwarp();
           last_bar = &empty[slot];
           last_ph = ph;
         };
@@ -507,10 +524,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
           open_segment(k, g, left);
           if (!g.empty) {
             const int n = g.todo;
-            ok = spin_wait_or_abort(&q_full, qph, abort_flag);
+            ok = wait_all(&q_full, qph, abort_flag);
             qph ^= 1u;
             for (int i = 0; ok && i < C::kAhead && i < n; ++i) {
-              ok = spin_wait_or_abort(&full[ri], rph, abort_flag);
+              ok = wait_all(&full[ri], rph, abort_flag);
               if (!ok) break;
               tc_fence_after();
               product_s(PAIR ? 0 : i, ri);
@@ -531,12 +548,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
               for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
                 const int s = PAIR ? u : (i & 1);
                 if (u == 0) {
-                  ok = cut ? spin_wait_or_abort(&tail[vs], (tph >> vs) & 1u, abort_flag)
-                           : spin_wait_or_abort(&full[vs], vph, abort_flag);
+                  ok = cut ? wait_all(&tail[vs], (tph >> vs) & 1u, abort_flag)
+                           : wait_all(&full[vs], vph, abort_flag);
                   if (!ok) break;
                   if (cut) tph ^= 1u << vs;
                 }
-                ok = spin_wait_or_abort(&p_full[s], (PAIR ? pph[u] : s ? pph[1] : pph[0]), abort_flag);
+                ok = wait_all(&p_full[s], (PAIR ? pph[u] : s ? pph[1] : pph[0]), abort_flag);
                 if (!ok) break;
                 if (PAIR)
                   pph[u] ^= 1u;
@@ -549,7 +566,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 if (u == (PAIR ? 1 : 0)) release(vs, vph);
                 if (more) {
                   if (u == 0) {
-                    ok = spin_wait_or_abort(&full[ks], kph, abort_flag);
+                    ok = wait_all(&full[ks], kph, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
                   }
@@ -559,7 +576,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
               }
             }
             if (!ok) break;
-            umma_commit(&q_empty);
+            if (lead) umma_commit(&q_empty);
+            __syncwarp();
           }
           advance();
         }
