@@ -86,16 +86,22 @@ __device__ __forceinline__ int seq_tiles(const TilePlan& p, const Seq& s) {
   return (s.n * p.group + p.rows - 1) / p.rows;
 }
 
-// Inclusive sum over the block's threads in thread order; `s_warp` holds one
-// int per warp.  Returns the inclusive sum, and the block's total in `total`.
-template <int NT>
-__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Inclusive sum over a warp's lanes.
+__device__ __forceinline__ int warp_scan(int v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
+  return v;
+}
+// Inclusive sum over the block's threads in thread order; `s_warp` holds one
+// int per warp.  Returns the inclusive sum, and the block's total in `total`.
+template <int NT>
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_scan(v);
   __syncthreads();  // s_warp may still be read from the call before
   if (lane == 31) s_warp[warp] = v;
   __syncthreads();
@@ -116,103 +122,81 @@ struct Start {
   int64_t units;               // units of this CTA (0: none)
 };
 
-constexpr int kMaxSeqs = 8192;
-
-// Called by all NT threads.  `s_nb`: at least n_seqs ints of shared memory,
-// free again when the call returns.
+// Called by all NT threads; every warp has the result.  `s_nb`: at least
+// n_seqs ints of shared memory, still read by other warps when the call
+// returns.  One barrier: the search stands before anything else of the call,
+// and of a small call it was the larger part (a form with a block-wide sum per
+// step took 5 us of the 70 us of a ragged batch of prompt chunks).
 template <int NT>
-__device__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int* s_nb) {
-  __shared__ int s_warp[NT / 32];
-  __shared__ int s_big[2], s_hit[3];
-  // Blocks of each sequence: one thread per sequence of few tiles, all
-  // threads for one of many.
-  int mine = 0;
-  for (int base = 0; base < b.n_seqs; base += NT) {
-    const int s = base + threadIdx.x;
+__device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int* s_nb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Blocks of each sequence: by its thread where it has one tile, else (left
+  // as -1) by a warp, a lane per tile.
+  for (int s0 = 32 * warp; s0 < b.n_seqs; s0 += NT) {
+    const int s = s0 + lane;
     int nb = 0;
     if (s < b.n_seqs) {
       const Seq q = load_seq(b, s);
       const int tiles = seq_tiles(p, q);
-      if (tiles <= 8) {
-        for (int i = 0; i < tiles; ++i) {
-          int f, c;
-          tile_blocks(p, q, i, f, c);
-          nb += c;
-        }
-      } else {
-        nb = -1;
-      }
+      int f;
+      if (tiles == 1) tile_blocks(p, q, 0, f, nb);
+      if (tiles > 1) nb = -1;
       s_nb[s] = nb;
     }
-    mine |= nb < 0;
-  }
-  if (__syncthreads_or(mine)) {
-    for (int s = 0; s < b.n_seqs; ++s) {
-      if (s_nb[s] >= 0) continue;  // the same for every thread
-      const Seq q = load_seq(b, s);
+    __syncwarp();
+    for (uint32_t more = __ballot_sync(0xffffffffu, nb < 0); more; more &= more - 1) {
+      const int t = s0 + __ffs(more) - 1;
+      const Seq q = load_seq(b, t);
       const int tiles = seq_tiles(p, q);
-      int nb = 0;
-      for (int i = threadIdx.x; i < tiles; i += NT) {
+      int sum = 0;
+      for (int i = lane; i < tiles; i += 32) {
         int f, c;
         tile_blocks(p, q, i, f, c);
-        nb += c;
+        sum += c;
       }
-      int total;
-      (void)block_scan<NT>(nb, s_warp, total);
-      if (threadIdx.x == 0) s_nb[s] = total;
-      __syncthreads();
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == 0) s_nb[t] = sum;
     }
   }
-  int64_t all = 0;  // blocks of one kv head
-  for (int base = 0; base < b.n_seqs; base += NT) {
-    const int s = base + threadIdx.x;
-    int total;
-    (void)block_scan<NT>(s < b.n_seqs ? s_nb[s] : 0, s_warp, total);
-    all += total;
-  }
+  __syncthreads();
+  // A lane per run of sequences: their sum, the sum of all, and the lane
+  // whose run holds the first unit.
+  const int run = (b.n_seqs + 31) >> 5, s0 = lane * run, s1 = min(s0 + run, b.n_seqs);
+  int mine = 0;
+  for (int s = s0; s < s1; ++s) mine += s_nb[s];
+  const int end = warp_scan(mine);
+  const int64_t all = __shfl_sync(0xffffffffu, end, 31);  // blocks of one kv head
   Start r;
   const int64_t work = all * n_kv;
   const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
   const int64_t u0 = cta < used ? work * cta / used : 0, u1 = cta < used ? work * (cta + 1) / used : 0;
   r.units = u1 - u0;
   r.head = r.seq = r.tile = r.block = 0;
-  if (r.units == 0) return r;  // the same for every thread
+  if (r.units == 0) return r;
   r.head = static_cast<int>(u0 / all);
   int rem = static_cast<int>(u0 - r.head * all);
-  int before = 0;
-  for (int base = 0; base < b.n_seqs; base += NT) {
-    const int s = base + threadIdx.x;
-    const int v = s < b.n_seqs ? s_nb[s] : 0;
-    int total;
-    const int end = before + block_scan<NT>(v, s_warp, total);
-    if (rem >= end - v && rem < end) {
-      s_big[0] = s;
-      s_big[1] = rem - (end - v);
-    }
-    before += total;
-    if (before > rem) break;  // the same for every thread
-  }
-  __syncthreads();
-  r.seq = s_big[0];
-  rem = s_big[1];
+  const int owner = __ffs(__ballot_sync(0xffffffffu, rem < end)) - 1;
+  int seq = s0;
+  int into = rem - (end - mine);
+  if (lane == owner)
+    while (into >= s_nb[seq]) into -= s_nb[seq++];
+  r.seq = __shfl_sync(0xffffffffu, seq, owner);
+  rem = __shfl_sync(0xffffffffu, into, owner);
   const Seq q = load_seq(b, r.seq);
   const int tiles = seq_tiles(p, q);
-  before = 0;
-  for (int base = 0; base < tiles; base += NT) {
-    const int i = base + threadIdx.x;
-    int f = 0, v = 0, total;
-    if (i < tiles) tile_blocks(p, q, i, f, v);
-    const int end = before + block_scan<NT>(v, s_warp, total);
-    if (rem >= end - v && rem < end) {
-      s_hit[0] = i;
-      s_hit[1] = rem - (end - v);
+  r.block = rem;
+  for (int base = 0; tiles > 1 && base < tiles; base += 32) {
+    int f, c = 0;
+    if (base + lane < tiles) tile_blocks(p, q, base + lane, f, c);
+    const int upto = warp_scan(c), sum = __shfl_sync(0xffffffffu, upto, 31);
+    if (rem < sum) {
+      const int hit = __ffs(__ballot_sync(0xffffffffu, rem < upto)) - 1;
+      r.tile = base + hit;
+      r.block = rem - __shfl_sync(0xffffffffu, upto - c, hit);
+      break;
     }
-    before += total;
-    if (before > rem) break;
+    rem -= sum;
   }
-  __syncthreads();
-  r.tile = s_hit[0];
-  r.block = s_hit[1];
   return r;
 }
 
