@@ -31,6 +31,7 @@ constexpr int kAWarps = 8, kAThreads = 32 * kAWarps;
 constexpr int kARows = 16;                // rows of a tile (one m16 operand)
 constexpr int kWarpKeys = 16;             // keys of a block per warp
 constexpr int kABlock = kWarpKeys * kAWarps;
+static_assert(kABlock == kBlockKeys, "a warp does 16 keys of every block");
 
 template <int D>
 struct WarpCfg {
@@ -112,8 +113,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
   const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTile;
   const float sc = a.scale * kLog2e;
   int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
-  Seq sq = load_seq(b, seq);
-  int64_t left = st.units;
+  Seq sq = st.sq;
+  int64_t left = st.units, unit = st.first;  // unit: of block blk
   for (bool first_seg = true;; first_seg = false) {
     int fb, nb;
     tile_blocks(plan, sq, tile, fb, nb);
@@ -299,16 +300,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
         *reinterpret_cast<float4*>(out + slot_o(kARows, r, col)) = v;
       }
     }
-    if (!whole && tid == 0) {
-      Part& p = parts[slot];
-      p.head = head;
-      p.q0 = sq.q0;
-      p.row0 = row0;
-      p.starts = blk == 0;
-      p.ends = blk + todo == nb;
-      p.rows = rows;
-    }
+    if (!whole && blk == 0 && tid == 0) parts[slot] = Part{head, sq.q0, row0, rows, share_of(st.work, st.used, unit + nb - 1), {}};
     left -= todo;
+    unit += todo;
     if (left == 0) break;
     __syncthreads();
     next_tile(plan, b, head, seq, tile, sq);
@@ -317,48 +311,69 @@ __global__ void __launch_bounds__(kAThreads, 1)
 }
 
 // Join the parts of the tiles that several CTAs did.  CTA (c, y) takes the
-// tile whose first part CTA c of the attention kernel left (if any) and the
-// y-th share of its rows; the parts that follow are the first ones of CTAs
-// c + 1, c + 2, ... up to the one that ends the tile.  Fixed order: the same
-// sums every time.
-template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    attn_join_kernel(const AttnArgs a, int slot_rows, int group, const Part* parts, const float* slots, int ctas) {
-  pdl_wait();
-  const int c = blockIdx.x;
-  int slot = -1;
-  for (int i = 0; i < 2; ++i) {
-    const Part& p = parts[2 * c + i];
-    if (p.rows > 0 && p.starts && !p.ends) slot = 2 * c + i;
+// tile whose first part CTA c of the attention kernel left (if any); the parts
+// that follow are the first ones of CTAs c + 1 .. last.  Many rows or few parts (prompt
+// chunks): a thread per piece of 4 columns.  Few rows in many parts (a decode
+// step over a long cache has one tile in 40): the CTA's warps share the parts
+// out, 32 pieces at a time, and their sums meet in shared memory.  Fixed
+// order: the same sums every time.
+constexpr int kJoinWarps = 8;
+
+struct RowSum {
+  float m, l;
+  float4 v;
+  __device__ __forceinline__ void add(float mk, float lk, float4 x) {
+    const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.0f : mn;
+    const float f0 = exp2f(m - base), f1 = exp2f(mk - base);
+    m = mn;
+    l = l * f0 + lk * f1;
+    v.x = v.x * f0 + x.x * f1;
+    v.y = v.y * f0 + x.y * f1;
+    v.z = v.z * f0 + x.z * f1;
+    v.w = v.w * f0 + x.w * f1;
   }
-  if (slot < 0) return;
-  const Part p = parts[slot];
-  int last = c + 1;
-  while (last < ctas && !parts[2 * last].ends) ++last;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    attn_join_kernel(const AttnArgs a, int slot_rows, int group, const Part* parts, const float* slots) {
+  __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
+  __shared__ float4 s_v[kJoinWarps][32];
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  const Part p0 = parts[2 * c], p1 = parts[2 * c + 1];
+  const bool second = p1.rows > 0;  // a CTA begins at most one tile that it does not end, its last
+  const Part p = second ? p1 : p0;
+  if (p.rows == 0) return;
   const size_t sf = join_slot_floats(slot_rows, D);
-  const int lrow = (slot_rows + 3) & ~3;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < p.rows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int r = e % p.rows, col = (e / p.rows) * 4;
-    const float* s = slots + slot * sf;
-    float m = s[r], l = s[lrow + r];
-    float4 v = *reinterpret_cast<const float4*>(s + slot_o(slot_rows, r, col));
+  const int lrow = (slot_rows + 3) & ~3, n = p.last - c + 1, items = p.rows * (D / 4);
+  const float* s0 = slots + (2 * c + second) * sf;
+  const bool many = n >= 4 && items <= static_cast<int>(64 * gridDim.y);
+  const int step = many ? 32 : 32 * kJoinWarps;
+  for (int base = blockIdx.y * step; base < items; base += gridDim.y * step) {
+    const int e = base + (many ? lane : static_cast<int>(threadIdx.x));
+    const bool there = e < items;
+    const int r = there ? e % p.rows : 0, col = there ? (e / p.rows) * 4 : 0, at = slot_o(slot_rows, r, col);
+    RowSum t = {-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
 #pragma unroll 4
-    for (int k = c + 1; k <= last && k < ctas; ++k) {
-      s = slots + 2 * k * sf;
-      const float mk = s[r], lk = s[lrow + r];
-      const float4 x = *reinterpret_cast<const float4*>(s + slot_o(slot_rows, r, col));
-      const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.0f : mn;
-      const float f0 = exp2f(m - base), f1 = exp2f(mk - base);
-      m = mn;
-      l = l * f0 + lk * f1;
-      v.x = v.x * f0 + x.x * f1;
-      v.y = v.y * f0 + x.y * f1;
-      v.z = v.z * f0 + x.z * f1;
-      v.w = v.w * f0 + x.w * f1;
+    for (int k = many ? warp : 0; k < n; k += many ? kJoinWarps : 1) {
+      const float* s = k == 0 ? s0 : slots + 2 * (c + k) * sf;
+      t.add(s[r], s[lrow + r], *reinterpret_cast<const float4*>(s + at));
     }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    if (many) {
+      __syncthreads();  // the sums of the pieces before have been read
+      s_m[warp][lane] = t.m;
+      s_l[warp][lane] = t.l;
+      s_v[warp][lane] = t.v;
+      __syncthreads();
+      if (warp > 0) continue;
+#pragma unroll
+      for (int w = 1; w < kJoinWarps; ++w) t.add(s_m[w][lane], s_l[w][lane], s_v[w][lane]);
+    }
+    if (!there) continue;
+    const float inv = t.l > 0.0f ? 1.0f / t.l : (t.l == 0.0f ? 0.0f : t.l);  // a row that sees nothing is zero
     const int tok = (p.row0 + r) / group, qh = p.head * group + (p.row0 + r) - tok * group;
-    store4<T>(a, p.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    store4<T>(a, p.q0 + tok, qh, D, col, make_float4(t.v.x * inv, t.v.y * inv, t.v.z * inv, t.v.w * inv));
   }
 }
 
@@ -404,7 +419,7 @@ int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, int ctas,
       return TQ1_ERR_CUDA;
     configured[di.device].store(true, std::memory_order_release);
   }
-  const TilePlan plan = {kARows, kABlock, a.n_q / c.n_kv, a.causal, a.window};
+  const TilePlan plan = {kARows, a.n_q / c.n_kv, a.causal, a.window};
   return launch_pdl(attn_warp_kernel<T, D>, dim3(ctas), kAThreads, C::kSmem, s, c, b, a, plan, parts, slots, status)
              ? TQ1_OK
              : TQ1_ERR_CUDA;
@@ -424,9 +439,9 @@ int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a,
   }
   if (rc != TQ1_OK) return rc;
   const int rows = route_rows(r, group);
-  const int share = (rows * (D / 4) + 1023) / 1024;  // four 4-column pieces a thread at most
-  return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 256, 0, s, a, rows, group, static_cast<const Part*>(parts),
-                    static_cast<const float*>(slots), ctas)
+  const int share = std::min(8, (rows * (D / 4) + 31) / 32);  // at most 8 CTAs an SM: all resident at once
+  return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 32 * kJoinWarps, 0, s, a, rows, group,
+                    static_cast<const Part*>(parts), static_cast<const float*>(slots))
              ? TQ1_OK
              : TQ1_ERR_CUDA;
 }

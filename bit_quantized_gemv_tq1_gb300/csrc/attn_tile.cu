@@ -28,10 +28,11 @@
 //
 // Roles: warps 0-3 and 4-7 the two streams' weights (a thread a row), warp 8
 // the matrix instructions, warp 9 the copies (TMA, a box per page and 64
-// elements, 128-byte swizzle).  Keys at or past a sequence's length are not
-// read at all where a whole page of them is, and otherwise warp 10 overwrites
-// their values with zeros in shared memory before the second product: a weight
-// of zero would not silence a NaN there.
+// elements, 128-byte swizzle), warp 10 walks the CTA's tiles for all of them.
+// Keys at or past a sequence's length are not read at all where a whole page
+// of them is, and otherwise warp 10 overwrites their values with zeros in
+// shared memory before the second product: a weight of zero would not silence
+// a NaN there.
 //
 // Every wait is bounded; the first that runs out sets an abort flag that
 // releases the others, and TQ1_ERR_TIMEOUT is raised.
@@ -46,11 +47,11 @@ namespace tq1 {
 
 namespace {
 
-constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;  // warp 11 makes the third warp group whole
+constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // warp 11 makes the third warp group whole
 // Registers per thread: 384 x 168 at launch = 2 x 128 x 208 + 128 x 88.
 constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
-constexpr int kTBlock = 128;  // keys of a block
+constexpr int kTBlock = kBlockKeys;
 constexpr float kMoveAt = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
 template <int D, bool PAIR>
@@ -61,7 +62,12 @@ struct TileCfg {
   static constexpr uint32_t kStatic = PAIR ? 1536 : 3584;      // barriers, and the streams' join
   static constexpr int kRing = static_cast<int>((232448 - kStatic - 1024) / kTile) - kQTiles;
   static constexpr uint32_t kSmem = (kQTiles + kRing) * kTile + 1024;
-  static constexpr int kAhead = PAIR ? 1 : 2;  // blocks of keys issued before a block's second product
+  // A stream's next block.  Blocks of keys are copied so many blocks ahead of
+  // their values, so a segment of n blocks fills its ring slots in the order
+  //   PAIR: K0 V0 K1 V1 K2 ...      else: K0 K1 V0 K2 V1 K3 V2 ...
+  static constexpr int kStep = PAIR ? 1 : 2;
+  static __device__ __forceinline__ uint32_t key_slot(int i) { return PAIR ? 2 * i : (i ? 2 * i - 1 : 0); }
+  static __device__ __forceinline__ uint32_t value_slot(int i, int n) { return PAIR ? 2 * i + 1 : i + min(i + 2, n); }
   static constexpr uint32_t kS = 0, kO = 256;  // tensor-memory columns: S of stream s at 128 s, O at kO + s D
 };
 
@@ -79,6 +85,7 @@ struct TileKernelArgs {
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   bool there = false;
+#pragma unroll 1
   for (int i = 0; i < 64 && !there; ++i) there = mbar_try_wait(bar, parity);
   if (!there) there = wait_or_abort(bar, parity, abort_flag);
   return __all_sync(0xffffffffu, there);  // the warp's lanes leave together, with one answer
@@ -88,6 +95,13 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_or_abort(bar, parity, abort_flag);
 }
 
 // Keys by elements (K order down the rows, 64 elements of N along a row):
@@ -161,27 +175,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return o;
 }
 
-// One tile's share of this CTA, as every role sees it.
+// One tile's share of this CTA, as the planning warp hands it to the others.
 struct Segment {
-  int head, seq, tile, blk, nb, todo;  // blocks [blk, blk + todo) of the tile's nb
-  int first_key;                       // of block blk
-  int row0, rows, tok0, hi;            // rows of the tile; first token; keys [.., hi) that some row sees
-  bool empty;                          // no row sees a key: nothing is read
-  Seq sq;
+  int head, seq, q0, len;  // kv head; sequence, its first token and its length
+  int pos0;                // position of its first token
+  int tok0, rows;          // first token and rows of the tile
+  int first_key, todo;     // blocks of the tile done here (0: no more segments)
+  int hi;                  // keys [.., hi) are seen by some row
+  int starts, ends;        // whether they include the tile's first, last block
+  int empty;               // no row sees a key: nothing is read
+  int last_cta;            // the CTA that does its last block
 };
-
-__device__ __forceinline__ void open_segment(const TileKernelArgs& k, Segment& g, int64_t left) {
-  int fb;
-  tile_blocks(k.plan, g.sq, g.tile, fb, g.nb);
-  g.todo = static_cast<int>(min(static_cast<int64_t>(g.nb - g.blk), left));
-  g.first_key = (fb + g.blk) * kTBlock;
-  g.row0 = g.tile * k.plan.rows;
-  g.rows = min(k.plan.rows, g.sq.n * k.plan.group - g.row0);
-  g.tok0 = g.row0 / k.plan.group;
-  const int last = (g.row0 + g.rows - 1) / k.plan.group, before = g.sq.len - g.sq.n;
-  g.hi = k.plan.causal ? min(g.sq.len, before + last + 1) : g.sq.len;
-  g.empty = g.hi <= (k.plan.window ? max(0, before + g.tok0 - k.plan.window + 1) : 0);
-}
+constexpr int kSegs = 4;            // segments in flight
+constexpr int kSegReaders = 8 + 2;  // warps that read them
 
 }  // namespace
 
@@ -192,7 +198,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
   using C = TileCfg<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing], tail[C::kRing];
-  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], swap;
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], swap, drained;
+  __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
+  __shared__ Segment s_seg[kSegs];
   __shared__ float s_ml[2][2][kTRows];  // [stream][m, l][row]: the streams' join
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
@@ -216,10 +224,15 @@ __global__ void __launch_bounds__(kTThreads, 1)
     mbar_init(&q_empty, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], kTRows);
+      mbar_init(&p_full[s], 4);
       mbar_init(&o_full[s], 1);
     }
-    mbar_init(&swap, 2 * kTRows);
+    mbar_init(&swap, 8);
+    mbar_init(&drained, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], kSegReaders);
+    }
     s_abort = 0;
     fence_mbar_init();
   }
@@ -238,21 +251,27 @@ __global__ void __launch_bounds__(kTThreads, 1)
   __syncthreads();
   if (tid < 2) k.parts[2 * cta + tid].rows = 0;
   __syncthreads();
+  // The next segment, for one of the reading warps; false after an abort.
+  uint32_t seg_at = 0;
   Segment g;
-  g.head = st.head;
-  g.seq = st.seq;
-  g.tile = st.tile;
-  g.blk = st.block;
-  int64_t left = st.units;
-  if (left > 0) g.sq = load_seq(k.b, g.seq);
-  auto advance = [&]() {
-    left -= g.todo;
-    if (left > 0) {
-      next_tile(k.plan, k.b, g.head, g.seq, g.tile, g.sq);
-      g.blk = 0;
-    }
+  auto next_segment = [&]() {
+    const uint32_t i = seg_at % kSegs;
+    if (!wait_all(&seg_full[i], (seg_at / kSegs) & 1u, abort_flag)) return false;
+    g = s_seg[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&seg_empty[i]);
+    ++seg_at;
+    return true;
   };
 
+  auto next_segment_one = [&]() {
+    const uint32_t i = seg_at % kSegs;
+    if (!wait_one(&seg_full[i], (seg_at / kSegs) & 1u, abort_flag)) return false;
+    g = s_seg[i];
+    mbar_arrive(&seg_empty[i]);
+    ++seg_at;
+    return true;
+  };
   if (warp < kMmaWarp) {
     // ---------------------------------------------------------- weights --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
@@ -261,20 +280,23 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const uint32_t st_at = tmem + lanes + C::kS + 128 * s, o_at = tmem + lanes + C::kO + s * D;
     const float sc = k.a.scale * kLog2e;
     uint32_t done = 0;   // blocks this stream has done, over all segments
+    uint32_t oph = 0;    // phase of o_full
     uint32_t swaps = 0;  // phases of `swap` passed
     bool ok = true;
-    for (bool first_seg = true; left > 0 && ok; first_seg = false) {
-      open_segment(k, g, left);
-      // This thread's row: its place in the tile, its keys [lo, hi).  Lanes
-      // past the stream's rows (or the sequence's) compute on what lies in
-      // shared memory and store nothing.
-      const int trow = PAIR ? s * k.stream_rows + row : row;
+    // This thread's row: its place in every tile (whole tokens, so its token
+    // and head in the tile are always the same).
+    const int trow = PAIR ? s * k.stream_rows + row : row;
+    const int ttok = trow / k.plan.group, thead = trow - ttok * k.plan.group;
+    for (bool first_seg = true; ok; first_seg = false) {
+      if (!next_segment() || g.todo == 0) break;
+      // The keys [lo, hi) that it sees.  Lanes past the stream's rows (or the
+      // sequence's) compute on what lies in shared memory and store nothing.
       const bool there = row < k.stream_rows && trow < g.rows;
-      const int tok = (g.row0 + trow) / k.plan.group, qh = g.head * k.plan.group + (g.row0 + trow) - tok * k.plan.group;
+      const int tok = g.tok0 + ttok, qh = g.head * k.plan.group + thead;
       int lo = 0, hi = 0x7fffffff;
       if (there) {
-        const int pos = g.sq.len - g.sq.n + tok;
-        hi = k.plan.causal ? min(g.sq.len, pos + 1) : g.sq.len;
+        const int pos = g.pos0 + tok;
+        hi = k.plan.causal ? min(g.len, pos + 1) : g.len;
         lo = k.plan.window ? max(0, pos - k.plan.window + 1) : 0;
       }
       float m = -INFINITY, l = 0.0f;  // the row's reference maximum (of S) and its sum
@@ -323,13 +345,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
                 m = mt;
                 l *= keep;
               }
-              // O is at rest once the block before has been added to it.
-              if (!wait_all(&o_full[s], (done - 1) & 1u, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-#pragma unroll
+              // O is at rest: the block before was added to it ahead of this S.
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld<32>(o_at + 32 * c, o);
@@ -363,14 +380,16 @@ __global__ void __launch_bounds__(kTThreads, 1)
           l += both.x + both.y;
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
-          mbar_arrive(&p_full[s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[s]);
           ++done;
         }
         if (!ok) break;
       }
       const bool mine = !g.empty && (PAIR || s < g.todo);  // this stream's O holds something
       if (mine) {
-        if (!wait_all(&o_full[s], (done - 1) & 1u, abort_flag)) break;
+        if (!wait_all(&o_full[s], oph, abort_flag)) break;
+        oph ^= 1u;
         tc_fence_after();
       }
       // Out: the row over its sum, or, of a tile that others share, the row
@@ -381,7 +400,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         s_ml[s][0][row] = mrow;
         s_ml[s][1][row] = l;
         tc_fence_before();
-        mbar_arrive(&swap);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&swap);
         if (!wait_all(&swap, swaps & 1u, abort_flag)) break;
         ++swaps;
         tc_fence_after();
@@ -391,13 +411,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
         f1 = m1 == -INFINITY ? 0.0f : exp2f(m1 - mrow);
         lrow = f0 * s_ml[0][1][row] + f1 * s_ml[1][1][row];
       }
-      const bool whole = g.blk == 0 && g.todo == g.nb;
+      const bool whole = g.starts && g.ends;
       const int slot = first_seg ? 2 * cta : 2 * cta + 1;
       float* out = k.slots + slot * join_slot_floats(k.plan.rows, D);
       const float inv = lrow > 0.0f ? 1.0f / lrow : (lrow == 0.0f ? 0.0f : lrow);  // a row that sees nothing is zero
-      const int64_t at = static_cast<int64_t>(g.sq.q0 + tok) * k.a.ldo + static_cast<int64_t>(qh) * D;
+      const int64_t at = static_cast<int64_t>(g.q0 + tok) * k.a.ldo + static_cast<int64_t>(qh) * D;
       constexpr int kCols = PAIR ? D : D / 2;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < kCols / 32; ++c) {
         const int col = (PAIR ? 0 : s * kCols) + 32 * c;
         float x[32];
@@ -442,165 +462,243 @@ __global__ void __launch_bounds__(kTThreads, 1)
           out[trow] = mrow;
           out[((k.plan.rows + 3) & ~3) + trow] = lrow;
         }
-        if (tid == 0) {
-          Part& p = k.parts[slot];
-          p.head = g.head;
-          p.q0 = g.sq.q0;
-          p.row0 = g.row0;
-          p.starts = g.blk == 0;
-          p.ends = g.blk + g.todo == g.nb;
-          p.rows = g.rows;
-        }
+        if (tid == 0 && g.starts) k.parts[slot] = Part{g.head, g.q0, g.tok0 * k.plan.group, g.rows, g.last_cta, {}};
       }
       if (!PAIR) {
         // The other stream has read this one's O and s_ml before either goes on.
         tc_fence_before();
-        mbar_arrive(&swap);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&swap);
         if (!wait_all(&swap, swaps & 1u, abort_flag)) break;
         ++swaps;
         tc_fence_after();
       }
-      advance();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA --
-      // In a step (a block's second product and the first product kAhead
-      // blocks on) the streams take turns.  The whole warp walks the loop and
-      // one lane issues: what the instructions take (descriptors, addresses)
-      // is then the same in all lanes to the compiler too, which keeps it in
-      // uniform registers instead of moving it there before each of them.
+      // In a step (a block's second product and the first product kStep
+      // blocks on) the streams take turns; issued from a warp each, their
+      // instructions would interleave and both streams' products finish late
+      // (670 us where this order takes 560: 4096 tokens on 12288 keys, 40/8
+      // heads of 128).  The whole warp walks the loop and one lane issues:
+      // what the instructions take (descriptors, addresses) is then the same
+      // in all lanes to the compiler too, which keeps it in uniform registers
+      // instead of moving it there before each of them (700 us).
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
       constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
-      const bool lead = elect_one();
-      {
-        uint32_t ri = 0, rph = 0;      // ring slot to be consumed next, its phase
-        uint32_t pph[2] = {0, 0};      // phases of p_full
-        uint32_t qph = 0, tph = 0;     // of q_full, and of each slot's tail (a bit per slot)
-        bool ok = true;
-        uint64_t* last_bar = nullptr;  // the latest release of a slot, for a clean end after an abort
-        uint32_t last_ph = 0;
-        const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
-        const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
-        auto step = [&]() {
-          if (++ri == C::kRing) {
-            ri = 0;
-            rph ^= 1u;
-          }
-        };
-        auto product_s = [&](int s, uint32_t slot) {
-          const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
-          if (lead) {
+      constexpr bool lead = true;
+      if (elect_one()) {
+      const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
+      const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
+      uint32_t pph = 0, qph = 0;   // phases of p_full (a bit per stream) and q_full
+      uint32_t tph = 0;            // and of each slot's tail (a bit per slot)
+      bool ok = true;
+      auto product_s = [&](int s, uint32_t slot) {
+        const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
+        if (lead) {
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
-              umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
-            }
-            umma_commit(&s_full[s]);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
+            umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
           }
-          __syncwarp();
-        };
-        auto product_o = [&](int s, uint32_t slot, int steps, uint32_t accumulate) {
-          const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
-          if (lead) {
+          umma_commit(&s_full[s]);
+        }
+      };
+      auto product_o = [&](int s, uint32_t slot, int steps, uint32_t keep) {
+        const uint32_t s_col = tmem + C::kS + 128 * s, o_col = tmem + C::kO + s * D;
+        const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
+        if (lead) {
+          if (steps == kTBlock / 16) {
 #pragma unroll
             for (int ks = 0; ks < kTBlock / 16; ++ks)
-              if (ks < steps)
-                umma_ts(tmem + C::kO + s * D, tmem + C::kS + 128 * s + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO,
-                        ks > 0 ? 1u : accumulate);
-            umma_commit(&o_full[s]);
+              umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
+          } else {
+            for (int ks = 0; ks < steps; ++ks)
+              umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
           }
-          __syncwarp();
-        };
-        auto release = [&](uint32_t slot, uint32_t ph) {
-          if (lead) umma_commit(&empty[slot]);
-          __syncwarp();
-          last_bar = &empty[slot];
-          last_ph = ph;
-        };
-        while (left > 0 && ok) {
-          open_segment(k, g, left);
-          if (!g.empty) {
-            const int n = g.todo;
-            ok = wait_all(&q_full, qph, abort_flag);
-            qph ^= 1u;
-            for (int i = 0; ok && i < C::kAhead && i < n; ++i) {
-              ok = wait_all(&full[ri], rph, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              product_s(PAIR ? 0 : i, ri);
-              if (PAIR) product_s(1, ri);
-              release(ri, rph);
-              step();
-            }
-            for (int i = 0; ok && i < n; ++i) {
-              const int key0 = g.first_key + i * kTBlock;
-              const int steps = (min(kTBlock, g.hi - key0) + 15) >> 4;
-              const bool cut = g.sq.len - key0 < 16 * steps;  // the tail warp has zeroed what lies past the end
-              const uint32_t vs = ri, vph = rph;
-              step();
-              const bool more = i + C::kAhead < n;
-              const uint32_t ks = ri, kph = rph;
-              if (more) step();
-#pragma unroll
-              for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
-                const int s = PAIR ? u : (i & 1);
-                if (u == 0) {
-                  ok = cut ? wait_all(&tail[vs], (tph >> vs) & 1u, abort_flag)
-                           : wait_all(&full[vs], vph, abort_flag);
-                  if (!ok) break;
-                  if (cut) tph ^= 1u << vs;
-                }
-                ok = wait_all(&p_full[s], (PAIR ? pph[u] : s ? pph[1] : pph[0]), abort_flag);
-                if (!ok) break;
-                if (PAIR)
-                  pph[u] ^= 1u;
-                else if (s)
-                  pph[1] ^= 1u;
-                else
-                  pph[0] ^= 1u;
-                tc_fence_after();
-                product_o(s, vs, steps, (PAIR ? i > 0 : i > 1) ? 1u : 0u);
-                if (u == (PAIR ? 1 : 0)) release(vs, vph);
-                if (more) {
-                  if (u == 0) {
-                    ok = wait_all(&full[ks], kph, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                  }
-                  product_s(s, ks);
-                  if (u == (PAIR ? 1 : 0)) release(ks, kph);
-                }
-              }
-            }
-            if (!ok) break;
-            if (lead) umma_commit(&q_empty);
-            __syncwarp();
-          }
-          advance();
         }
-        // After an abort, let the products already issued finish (bounded).
-        if (*abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lead) umma_commit(bar);
+      };
+      uint32_t ri = 0, rph = 0;
+      auto step = [&]() {
+        if (++ri == C::kRing) {
+          ri = 0;
+          rph ^= 1u;
+        }
+      };
+      while (ok && next_segment_one() && g.todo > 0) {
+        if (g.empty) continue;
+        const int n = g.todo;
+        if (!(ok = wait_one(&q_full, qph, abort_flag))) break;
+        qph ^= 1u;
+        for (int i = 0; i < C::kStep && i < n; ++i) {
+          if (!(ok = wait_one(&full[ri], rph, abort_flag))) break;
+          tc_fence_after();
+          product_s(PAIR ? 0 : i, ri);
+          if (PAIR) product_s(1, ri);
+          commit(&empty[ri]);
+          step();
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const bool more = i + C::kStep < n;
+          if (i + C::kStep == n || (i == 0 && n < C::kStep)) commit(&q_empty);  // the last first product is on its way
+          const int key0 = g.first_key + i * kTBlock;
+          const int steps = (min(kTBlock, g.hi - key0) + 15) >> 4;
+          const uint32_t slot = ri, sph = rph;
+          step();
+          const uint32_t nslot = ri, nph = rph;
+          if (more) step();
+          if (g.len - key0 < 16 * steps) {  // what lies past the end is zeroed first
+            ok = wait_one(&tail[slot], (tph >> slot) & 1u, abort_flag);
+            tph ^= 1u << slot;
+          } else {
+            ok = wait_one(&full[slot], sph, abort_flag);
+          }
+          if (ok && more) ok = wait_one(&full[nslot], nph, abort_flag);
+#pragma unroll
+          for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
+            const int s = PAIR ? u : (i & 1);
+            if (!ok || !(ok = wait_one(&p_full[s], (pph >> s) & 1u, abort_flag))) break;
+            pph ^= 1u << s;
+            tc_fence_after();
+            product_o(s, slot, steps, i >= C::kStep ? 1u : 0u);
+            if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
+            if (more) {
+              product_s(s, nslot);
+              if (u == (PAIR ? 1 : 0)) umma_commit(&empty[nslot]);
+            } else {
+              umma_commit(&o_full[s]);
+            }
+          }
+        }
       }
-    } else if (warp == kTailWarp) {
-      // ---------------------------------------------------------- tails --
-      // Zeros over the values past a sequence's end, up to the end of the
-      // last group of 16 that is multiplied.  The last values of a segment
-      // are its last ring slot.  A barrier per slot: the slot is not filled
-      // again before its products are done, so no phase can be missed.
-      uint32_t slots_done = 0;
+      // After an abort, let the products already issued finish (bounded).
+      if (*abort_flag) {
+        commit(&drained);
+        (void)mbar_wait(&drained, 0);
+      }
+      }
+    } else if (warp == kLoadWarp) {
+      // --------------------------------------------------------- copies --
+      uint32_t at = 0, segs = 0;  // ring slots filled, segments read
       bool ok = true;
-      while (left > 0 && ok) {
-        open_segment(k, g, left);
-        if (!g.empty) {
-          const uint32_t at = slots_done + 2 * g.todo - 1, slot = at % C::kRing, ph = (at / C::kRing) & 1u;
-          slots_done += 2 * g.todo;
-          const int key0 = g.first_key + (g.todo - 1) * kTBlock;
-          const int upto = (min(kTBlock, g.hi - key0) + 15) & ~15, from = g.sq.len - key0;
+      const int boxes = kTBlock / k.box_keys;  // of a block
+      const int half = lane & (D / 64 - 1), box = lane / (D / 64);
+      // The page of this lane's box of the block from key0 on: -1 (read as
+      // zeros) where the table names none, -2 past the sequence's end.
+      auto page_of = [&](int key0) {
+        const int key = key0 + box * k.box_keys;
+        if (box >= boxes || key >= g.len) return -2;
+        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
+        if (id >= 0 && id < k.c.n_pages) return id;
+        raise_status(k.status, kStatusBadId);
+        return -1;
+      };
+      auto copy = [&](const CUtensorMap* map, int key0, int page) {
+        const uint32_t slot = at % C::kRing;
+        if (!(ok = wait_all(&empty[slot], ((at / C::kRing) & 1u) ^ 1u, abort_flag))) return false;
+        const uint32_t live = __ballot_sync(0xffffffffu, page != -2);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * k.box_keys * 128);
+        __syncwarp();
+        if (page != -2)
+          tma_load_4d(ring_at + slot * C::kTile + half * C::kHalf + box * k.box_keys * 128, map, 64 * half,
+                      (key0 + box * k.box_keys) & (k.c.page_size - 1), g.head, page, &full[slot]);
+        ++at;
+        return true;
+      };
+      while (ok && next_segment() && g.todo > 0) {
+        if (g.empty) continue;
+        int page[C::kStep];
+#pragma unroll
+        for (int i = 0; i < C::kStep; ++i) page[i] = i < g.todo ? page_of(g.first_key + i * kTBlock) : -2;
+        if (!(ok = wait_all(&q_empty, (segs & 1u) ^ 1u, abort_flag))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, C::kQTiles * (D / 64) * k.stream_rows * 128);
+        __syncwarp();
+        if (lane < C::kQTiles * (D / 64)) {
+          const int qs = lane / (D / 64), qhalf = lane & (D / 64 - 1);
+          tma_load_3d(q_at + qs * C::kTile + qhalf * C::kHalf, &tmq, 64 * qhalf, g.head * k.plan.group,
+                      g.q0 + g.tok0 + qs * k.stream_tokens, &q_full);
+        }
+        ++segs;
+        for (int i = 0; i < C::kStep && i < g.todo && ok; ++i) copy(&tmk, g.first_key + i * kTBlock, page[i]);
+        for (int i = 0; i < g.todo && ok; ++i) {
+          const int next = i + C::kStep, key = g.first_key + i * kTBlock;
+          const int np = next < g.todo ? page_of(g.first_key + next * kTBlock) : -2;
+          if (!copy(&tmv, key, page[0])) break;
+          if (next < g.todo && !copy(&tmk, g.first_key + next * kTBlock, np)) break;
+#pragma unroll
+          for (int j = 0; j + 1 < C::kStep; ++j) page[j] = page[j + 1];
+          page[C::kStep - 1] = np;
+        }
+      }
+      // Copies still in flight must land before the CTA leaves.
+      if (lane == 0 && *abort_flag) {
+        for (uint32_t i = at > C::kRing ? at - C::kRing : 0; i < at; ++i)
+          (void)mbar_wait(&full[i % C::kRing], (i / C::kRing) & 1u);
+        if (segs) (void)mbar_wait(&q_full, (segs - 1) & 1u);
+      }
+    } else if (warp == kPlanWarp) {
+      // ------------------------------------------------- plan and tails --
+      // Hands out the segments, one ahead of the one whose tail it tends:
+      // zeros over the values past a sequence's end, up to the end of the
+      // last group of 16 that is multiplied.  A segment's last values are its
+      // last ring slot.  A barrier per slot: the slot is not filled again
+      // before its products are done, so no phase can be missed.
+      Segment last = {};
+      uint32_t slots_done = 0;
+      int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
+      int64_t left = st.units, unit = st.first;
+      Seq sq = st.sq;
+      for (bool more = true; more; ++seg_at) {
+        g = Segment{};
+        more = left > 0;
+        if (more) {
+          int fb, nb;
+          tile_blocks(k.plan, sq, tile, fb, nb);
+          const int row0 = tile * k.plan.rows;
+          g.head = head;
+          g.seq = seq;
+          g.q0 = sq.q0;
+          g.len = sq.len;
+          g.pos0 = sq.len - sq.n;
+          g.tok0 = row0 / k.plan.group;
+          g.rows = min(k.plan.rows, sq.n * k.plan.group - row0);
+          g.first_key = (fb + blk) * kTBlock;
+          g.todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
+          const int end = row0 + g.rows;
+          g.hi = k.plan.causal ? min(sq.len, g.pos0 + (end - 1) / k.plan.group + 1) : sq.len;
+          g.empty = g.hi <= (k.plan.window ? max(0, g.pos0 + g.tok0 - k.plan.window + 1) : 0);
+          g.starts = blk == 0;
+          g.ends = blk + g.todo == nb;
+          if (g.starts && !g.ends) g.last_cta = share_of(st.work, st.used, unit + nb - 1);
+        }
+        const uint32_t i = seg_at % kSegs;
+        if (!wait_all(&seg_empty[i], ((seg_at / kSegs) & 1u) ^ 1u, abort_flag)) break;
+        if (lane == 0) {
+          s_seg[i] = g;
+          mbar_arrive(&seg_full[i]);
+        }
+        __syncwarp();
+        if (more) {
+          left -= g.todo;
+          unit += g.todo;
+          if (left > 0) {
+            next_tile(k.plan, k.b, head, seq, tile, sq);
+            blk = 0;
+          }
+        }
+        if (last.todo > 0 && !last.empty) {
+          const uint32_t at = slots_done + 2 * last.todo - 1, slot = at % C::kRing;
+          slots_done += 2 * last.todo;
+          const int key0 = last.first_key + (last.todo - 1) * kTBlock;
+          const int upto = (min(kTBlock, last.hi - key0) + 15) & ~15, from = last.len - key0;
           if (from < upto) {
-            if (!(ok = wait_all(&full[slot], ph, abort_flag))) break;
+            if (!wait_all(&full[slot], (at / C::kRing) & 1u, abort_flag)) break;
             for (int r = from; r < upto; ++r)
               for (int c = lane; c < (D / 64) * 8; c += 32)
                 *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 +
@@ -610,79 +708,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
             if (lane == 0) mbar_arrive(&tail[slot]);
           }
         }
-        advance();
+        last = g;
       }
-    } else if (warp == kLoadWarp) {
-      // ----------------------------------------------------------- copies --
-      uint32_t ri = 0, rph = 0, segs = 0;
-      bool ok = true;
-      uint64_t* last_bar = nullptr;
-      uint32_t last_ph = 0;
-      const int boxes = kTBlock / k.box_keys;  // of a block
-      const int half = lane & (D / 64 - 1), box = lane / (D / 64);
-      auto take = [&](uint64_t* bar, uint32_t ph) {
-        int r = 1;
-        if (lane == 0) r = wait_or_abort(bar, ph, abort_flag) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, r, 0) != 0;
-        return ok;
-      };
-      // The page of this lane's box of the block from key0 on: -1 (read as
-      // zeros) where the table names none, -2 past the sequence's end.
-      auto page_of = [&](int key0) {
-        const int key = key0 + box * k.box_keys;
-        if (box >= boxes || key >= g.sq.len) return -2;
-        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
-        if (id >= 0 && id < k.c.n_pages) return id;
-        raise_status(k.status, kStatusBadId);
-        return -1;
-      };
-      auto copy = [&](const CUtensorMap* map, int key0, int page) {
-        if (!take(&empty[ri], rph ^ 1u)) return false;
-        const uint32_t live = __ballot_sync(0xffffffffu, page != -2);
-        if (lane == 0) mbar_arrive_expect_tx(&full[ri], __popc(live) * k.box_keys * 128);
-        __syncwarp();
-        if (page != -2)
-          tma_load_4d(ring_at + ri * C::kTile + half * C::kHalf + box * k.box_keys * 128, map, 64 * half,
-                      (key0 + box * k.box_keys) & (k.c.page_size - 1), g.head, page, &full[ri]);
-        last_bar = &full[ri];
-        last_ph = rph;
-        if (++ri == C::kRing) {
-          ri = 0;
-          rph ^= 1u;
-        }
-        return true;
-      };
-      while (left > 0 && ok) {
-        open_segment(k, g, left);
-        if (!g.empty) {
-          int page[C::kAhead];
-  #pragma unroll
-          for (int i = 0; i < C::kAhead; ++i) page[i] = i < g.todo ? page_of(g.first_key + i * kTBlock) : -2;
-          if (!take(&q_empty, (segs & 1u) ^ 1u)) break;
-          if (lane == 0) mbar_arrive_expect_tx(&q_full, C::kQTiles * (D / 64) * k.stream_rows * 128);
-          __syncwarp();
-          if (lane < C::kQTiles * (D / 64)) {
-            const int qs = lane / (D / 64), qhalf = lane & (D / 64 - 1);
-            tma_load_3d(q_at + qs * C::kTile + qhalf * C::kHalf, &tmq, 64 * qhalf, g.head * k.plan.group,
-                        g.sq.q0 + g.tok0 + qs * k.stream_tokens, &q_full);
-          }
-          ++segs;
-          for (int i = 0; i < C::kAhead && i < g.todo && ok; ++i) copy(&tmk, g.first_key + i * kTBlock, page[i]);
-          for (int i = 0; i < g.todo && ok; ++i) {
-            const int next = i + C::kAhead, key = g.first_key + i * kTBlock;
-            const int np = next < g.todo ? page_of(g.first_key + next * kTBlock) : -2;
-            if (!copy(&tmv, key, page[0])) break;
-            if (next < g.todo && !copy(&tmk, g.first_key + next * kTBlock, np)) break;
-  #pragma unroll
-            for (int j = 0; j + 1 < C::kAhead; ++j) page[j] = page[j + 1];
-            page[C::kAhead - 1] = np;
-          }
-          if (!ok) break;
-        }
-        advance();
-      }
-      // Copies still in flight must land before the CTA leaves.
-      if (lane == 0 && *abort_flag && last_bar) (void)mbar_wait(last_bar, last_ph);
     }
   }
   __syncthreads();
@@ -747,7 +774,7 @@ int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool
   k.c = c;
   k.b = b;
   k.a = a;
-  k.plan = {attn_tile_rows(group, pair), kTBlock, group, a.causal, a.window};
+  k.plan = {attn_tile_rows(group, pair), group, a.causal, a.window};
   k.parts = parts;
   k.slots = slots;
   k.status = status;

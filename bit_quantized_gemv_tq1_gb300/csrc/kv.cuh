@@ -66,8 +66,9 @@ __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
 // [W c / C, W (c+1) / C) of the W in the list.  So every CTA has the same
 // work to one unit whatever the sequences' lengths are, and only the tiles at
 // a CTA's two ends are shared: their parts are joined afterwards.
+constexpr int kBlockKeys = 128;
 struct TilePlan {
-  int rows, block, group, causal, window;
+  int rows, group, causal, window;
 };
 
 // Blocks of one tile: the first one and how many.  A tile whose rows see
@@ -78,8 +79,8 @@ __device__ __forceinline__ void tile_blocks(const TilePlan& p, const Seq& s, int
   const int pos0 = s.len - s.n + tok0, pos1 = s.len - s.n + tok1;
   const int hi = p.causal ? min(s.len, pos1 + 1) : s.len;
   const int lo = p.window ? max(0, pos0 - p.window + 1) : 0;
-  first = lo / p.block;
-  count = max(1, (hi + p.block - 1) / p.block - first);
+  first = lo / kBlockKeys;
+  count = max(1, (hi + kBlockKeys - 1) / kBlockKeys - first);
   if (hi <= lo) count = 1;
 }
 __device__ __forceinline__ int seq_tiles(const TilePlan& p, const Seq& s) {
@@ -119,8 +120,26 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
 // Where CTA `cta` of `ctas` begins and how much it does.
 struct Start {
   int head, seq, tile, block;  // first unit
-  int64_t units;               // units of this CTA (0: none)
+  int64_t first, units;        // its place in the list, units of this CTA (0: none)
+  int64_t work;                // units of the call
+  int used;                    // CTAs that have some
+  Seq sq;                      // of `seq`
 };
+
+// Unit u0 of share c of `work` units over `used` shares, and the share that
+// has unit u.
+__device__ __forceinline__ int64_t share_begin(int64_t work, int used, int c) {
+  if (work < (int64_t{1} << 31)) {  // 32-bit divisions: a 64-bit one takes some hundred instructions
+    const uint32_t q = static_cast<uint32_t>(work) / static_cast<uint32_t>(used), r = static_cast<uint32_t>(work) - q * used;
+    return static_cast<int64_t>(q) * c + min(static_cast<uint32_t>(c), r);
+  }
+  const int64_t q = work / used, r = work - q * used;
+  return q * c + min(static_cast<int64_t>(c), r);
+}
+__device__ __forceinline__ int share_of(int64_t work, int used, int64_t u) {
+  const int64_t q = work / used, r = work - q * used, longer = (q + 1) * r;
+  return static_cast<int>(u < longer ? u / (q + 1) : r + (u - longer) / q);
+}
 
 // Called by all NT threads; every warp has the result.  `s_nb`: at least
 // n_seqs ints of shared memory, still read by other warps when the call
@@ -169,12 +188,17 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   Start r;
   const int64_t work = all * n_kv;
   const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
-  const int64_t u0 = cta < used ? work * cta / used : 0, u1 = cta < used ? work * (cta + 1) / used : 0;
-  r.units = u1 - u0;
+  r.work = work;
+  r.used = used;
+  r.first = 0;
+  r.units = 0;
   r.head = r.seq = r.tile = r.block = 0;
-  if (r.units == 0) return r;
-  r.head = static_cast<int>(u0 / all);
-  int rem = static_cast<int>(u0 - r.head * all);
+  r.sq = Seq{0, 0, 0};
+  if (cta >= used) return r;
+  r.first = share_begin(work, used, cta);
+  r.units = share_begin(work, used, cta + 1) - r.first;
+  r.head = work < (int64_t{1} << 31) ? static_cast<uint32_t>(r.first) / static_cast<uint32_t>(all) : static_cast<int>(r.first / all);
+  int rem = static_cast<int>(r.first - r.head * all);
   const int owner = __ffs(__ballot_sync(0xffffffffu, rem < end)) - 1;
   int seq = s0;
   int into = rem - (end - mine);
@@ -183,6 +207,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   r.seq = __shfl_sync(0xffffffffu, seq, owner);
   rem = __shfl_sync(0xffffffffu, into, owner);
   const Seq q = load_seq(b, r.seq);
+  r.sq = q;
   const int tiles = seq_tiles(p, q);
   r.block = rem;
   for (int base = 0; tiles > 1 && base < tiles; base += 32) {
@@ -219,9 +244,10 @@ __device__ __forceinline__ void next_tile(const TilePlan& p, const KvBatch& b, i
 // What a CTA left of a tile it did not do alone (its first or its last):
 // rows of m, l and unnormalised O in the workspace, described by a Part.
 struct Part {
-  int head, q0, row0, rows;  // kv head, first token of the sequence, first row of the tile, rows (0: no part)
-  int starts, ends;          // whether the part has the tile's first / last block
-  int pad[2];
+  int head, q0, row0;  // kv head, first token of the sequence, first row of the tile
+  int rows;            // rows, in the part with the tile's first block; 0 in the others and where there is none
+  int last;            // the CTA that has the tile's last block
+  int pad[3];
 };
 
 // Workspace of `ctas` CTAs: their parts, then two slots each of rows * (d + 2)
