@@ -20,5 +20,6 @@ __all__ = list(_EXPORTS)
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # looked up here once
+        return value
     raise AttributeError(name)

@@ -64,6 +64,8 @@ def library_path() -> str:
 def library() -> ctypes.CDLL:
     """Load libtq1.so (must have been built by build.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -153,10 +155,29 @@ def _addr(x) -> int | None:
     return x.data_ptr()
 
 
+def _current_stream():
+    """A function that returns the address of the current device's current stream."""
+    import torch
+    try:  # the address alone: building a Stream object takes 3 us, as long as a small call's kernels
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    except AttributeError:
+        return lambda: torch.cuda.current_stream().cuda_stream
+
+    def current() -> int:
+        torch.cuda._lazy_init()
+        return raw(device())
+    return current
+
+
+_current = None
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current
+        if _current is None:
+            _current = _current_stream()
+        return _current()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -338,33 +359,49 @@ def tq1_sync_status(stream=None) -> int:
 
 
 # ------------------------------------------------ paged key/value cache --
+_dtypes = None
+
+
 def _dtype(x) -> int:
-    import torch
-    try:
-        return {torch.float32: TQ1_F32, torch.float16: TQ1_F16, torch.bfloat16: TQ1_BF16}[x.dtype]
-    except KeyError:
-        raise ValueError(f"libtq1 takes fp32, fp16 and bf16 here, not {x.dtype}") from None
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.float32: TQ1_F32, torch.float16: TQ1_F16, torch.bfloat16: TQ1_BF16}
+    code = _dtypes.get(x.dtype)
+    if code is None:
+        raise ValueError(f"libtq1 takes fp32, fp16 and bf16 here, not {x.dtype}")
+    return code
+
+
+_int32 = None
 
 
 def _ints(x, n: int | None = None) -> int:
     """Device address of a contiguous int32 tensor (of n elements)."""
-    import torch
-    if x.dtype != torch.int32:
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    if x.dtype is not _int32:
         raise ValueError(f"libtq1 takes int32 indexes, not {x.dtype}")
     if n is not None and x.numel() != n:
         raise ValueError(f"expected {n} values, got {x.numel()}")
     return _addr(x)
 
 
-def _rows(x, heads: int | None, d: int, what: str) -> tuple[int, int]:
-    """Address and token stride (elements) of [t][heads][d] rows, e.g. a column range of a fused projection."""
-    if x.dim() != 3 or x.shape[2] != d or (heads is not None and x.shape[1] != heads):
-        raise ValueError(f"{what}: expected [t][{heads or 'heads'}][{d}], got {tuple(x.shape)}")
+def _rows(x, heads: int | None, d: int, what: str) -> tuple[int, int, int, int]:
+    """Address, token stride (elements), tokens and heads of [t][heads][d] rows, e.g. a column range of a fused
+    projection."""
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{what}: expected [t][{heads or 'heads'}][{d}], got {tuple(shape)}")
     if not x.is_cuda:
         raise ValueError("libtq1 takes CUDA tensors only")
-    if x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != d):
+    t, n, _ = shape
+    st, sh, se = x.stride()
+    if se != 1 or (n > 1 and sh != d):
         raise ValueError(f"{what}: a token's heads must be contiguous")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1] * d
+    return x.data_ptr(), st if t > 1 else n * d, t, n
 
 
 def tq1_kv_cache(k, v) -> KvCache:
@@ -403,17 +440,19 @@ def tq1_rope_freqs(inv_freq, rot_dim: int, base: float = 10000.0, factor: float 
 def tq1_rope_append(cache, batch, q, k, v, q_out, inv_freq, rot_dim: int, interleaved: bool = False,
                     mscale: float = 1.0, positions=None, stream=None) -> None:
     """Rotate q [t][n_q][d] into q_out and append the rotated k and the v [t][n_kv][d] to the cache's pages."""
-    t, n_q, d, n_kv = q.shape[0], q.shape[1], cache.head_dim, cache.n_kv
-    (pq, ldq), (pk, ldk), (pv, ldv) = _rows(q, None, d, "q"), _rows(k, n_kv, d, "k"), _rows(v, n_kv, d, "v")
-    if k.shape[0] != t or v.shape[0] != t or not (q.dtype == k.dtype == v.dtype):
+    d, n_kv = cache.head_dim, cache.n_kv
+    pq, ldq, t, n_q = _rows(q, None, d, "q")
+    pk, ldk, tk, _ = _rows(k, n_kv, d, "k")
+    pv, ldv, tv, _ = _rows(v, n_kv, d, "v")
+    if tk != t or tv != t or not (q.dtype is k.dtype is v.dtype):
         raise ValueError("q, k and v: one type and one number of tokens")
-    if tuple(q_out.shape) != (t, n_q, d) or _dtype(q_out) != cache.dtype:
+    if q_out.shape != q.shape or _dtype(q_out) != cache.dtype:
         raise ValueError("q_out: q's shape and the cache's type")
     if inv_freq is not None and (inv_freq.numel() != rot_dim // 2 or _dtype(inv_freq) != TQ1_F32):
         raise ValueError(f"inv_freq: expected {rot_dim // 2} fp32 values")
     pos = None if positions is None else _ints(positions, t)
     _check(library().tq1_rope_append(cache, batch, pq, ldq, pk, ldk, pv, ldv, _dtype(q), _addr(q_out), t, n_q,
-                                     _addr(inv_freq), rot_dim, int(bool(interleaved)), mscale, pos, _stream(stream)),
+                                     _addr(inv_freq), rot_dim, 1 if interleaved else 0, mscale, pos, _stream(stream)),
            "tq1_rope_append")
 
 
@@ -424,13 +463,14 @@ def tq1_paged_attn_workspace_size(cache, t: int, n_q: int, n_seqs: int) -> int:
 def tq1_paged_attn(cache, batch, q, out, scale: float, causal: bool = True, window: int = 0, ws=None,
                    ws_bytes: int | None = None, stream=None) -> None:
     """out [t][n_q][d] (the cache's type, or fp32) = attention of q [t][n_q][d] over the batch's pages."""
-    t, n_q, d = q.shape[0], q.shape[1], cache.head_dim
-    (pq, ldq), (po, ldo) = _rows(q, None, d, "q"), _rows(out, n_q, d, "out")
-    if out.shape[0] != t or _dtype(q) != cache.dtype or _dtype(out) not in (cache.dtype, TQ1_F32):
+    d, dtype, out_dtype = cache.head_dim, cache.dtype, _dtype(out)
+    pq, ldq, t, n_q = _rows(q, None, d, "q")
+    po, ldo, to, _ = _rows(out, n_q, d, "out")
+    if to != t or _dtype(q) != dtype or (out_dtype != dtype and out_dtype != TQ1_F32):
         raise ValueError("q: the cache's type; out: q's shape, the cache's type or fp32")
     wsb = ws_bytes if ws_bytes is not None else (0 if ws is None else ws.numel() * ws.element_size())
-    _check(library().tq1_paged_attn(cache, batch, pq, ldq, t, n_q, scale, int(bool(causal)), window, po, ldo,
-                                    int(_dtype(out) == TQ1_F32), _addr(ws), wsb, _stream(stream)), "tq1_paged_attn")
+    _check(library().tq1_paged_attn(cache, batch, pq, ldq, t, n_q, scale, 1 if causal else 0, window, po, ldo,
+                                    1 if out_dtype == TQ1_F32 else 0, _addr(ws), wsb, _stream(stream)), "tq1_paged_attn")
 
 
 def tq1_page_pool(pools, page_table, kv_len, refs, page_size: int) -> PagePool:
