@@ -39,10 +39,10 @@ struct PagesWs {
   int32_t* dst;     // [n_pages]
   int32_t* rank;    // [n_pages]   compaction: place of a moving page in the list
   int32_t* chunks;  // [ceil(n_pages / kChunkPages)] live pages per chunk
-  int32_t* need;    // [n_seqs]    pages wanted before argument i; [n_seqs] flags follow
+  int32_t* left;    // [n_seqs]    the page that argument i leaves for a copy of its own, or -1
 };
 __host__ __device__ inline size_t pages_words(int64_t n_pages, int64_t n_seqs) {
-  return 64 + 3 * static_cast<size_t>(n_pages) + (n_pages + kChunkPages - 1) / kChunkPages + 2 * static_cast<size_t>(n_seqs);
+  return 64 + 3 * static_cast<size_t>(n_pages) + (n_pages + kChunkPages - 1) / kChunkPages + static_cast<size_t>(n_seqs);
 }
 inline PagesWs split_ws(void* ws, int64_t n_pages) {
   PagesWs w;
@@ -51,58 +51,78 @@ inline PagesWs split_ws(void* ws, int64_t n_pages) {
   w.dst = w.src + n_pages;
   w.rank = w.dst + n_pages;
   w.chunks = w.rank + n_pages;
-  w.need = w.chunks + (n_pages + kChunkPages - 1) / kChunkPages;
+  w.left = w.chunks + (n_pages + kChunkPages - 1) / kChunkPages;
   return w;
 }
 
 __device__ __forceinline__ int up(int a, int b) { return (a + b - 1) / b; }
 
-// The lowest `want` free pages into `out`, ascending, by the whole CTA; the
-// scan stops as soon as it has them.  Returns how many there were (<= want).
-__device__ int find_free(const int32_t* refs, int n_pages, int want, int32_t* out, int* s_warp) {
+// This thread's four counts of the chunk of pages from `base` on; pages past
+// the end are in use.
+__device__ __forceinline__ int4 load_refs(const int32_t* refs, int n_pages, int base) {
+  const int p = base + 4 * static_cast<int>(threadIdx.x);
+  if (p + 3 < n_pages) return __ldcg(reinterpret_cast<const int4*>(refs + p));
+  int4 r = make_int4(1, 1, 1, 1);
+  if (p < n_pages) r.x = __ldcg(refs + p);
+  if (p + 1 < n_pages) r.y = __ldcg(refs + p + 1);
+  if (p + 2 < n_pages) r.z = __ldcg(refs + p + 2);
+  return r;
+}
+
+// The lowest `want` free pages into `out`, ascending, by the whole CTA, which
+// holds the first chunk's counts in `r`; the scan stops as soon as it has
+// them.  Returns how many there were (<= want).
+__device__ int find_free(const int32_t* refs, int n_pages, int want, int4 r, int32_t* out, int* s_warp) {
   int found = 0;
-  for (int base = 0; base < n_pages && found < want; base += kChunkPages) {
-    const int p0 = base + 4 * threadIdx.x;
-    int r[4] = {1, 1, 1, 1};
-    if (p0 + 3 < n_pages) {
-      const int4 v = __ldcg(reinterpret_cast<const int4*>(refs + p0));
-      r[0] = v.x;
-      r[1] = v.y;
-      r[2] = v.z;
-      r[3] = v.w;
-    } else {
-      for (int i = 0; i < 4; ++i)
-        if (p0 + i < n_pages) r[i] = __ldcg(refs + p0 + i);
-    }
-    const int mine = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
+  for (int base = 0;;) {
+    const int mine = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
     int total;
     int at = found + block_scan<kPlanThreads>(mine, s_warp, total) - mine;
-    for (int i = 0; i < 4; ++i)
-      if (r[i] == 0) {
-        if (at < want) out[at] = p0 + i;
-        ++at;
-      }
+    const int p = base + 4 * static_cast<int>(threadIdx.x);
+    if (r.x == 0 && at++ < want) out[at - 1] = p;
+    if (r.y == 0 && at++ < want) out[at - 1] = p + 1;
+    if (r.z == 0 && at++ < want) out[at - 1] = p + 2;
+    if (r.w == 0 && at++ < want) out[at - 1] = p + 3;
     found += total;
+    base += kChunkPages;
+    if (found >= want || base >= n_pages) break;
+    r = load_refs(refs, n_pages, base);
   }
   __syncthreads();
   return min(found, want);
 }
 
-// Exclusive sums of need[i] (n values, in place), by the whole CTA; returns
-// their total, at most 2^30.
-__device__ int sum_needs(int32_t* need, int n, int* s_warp) {
-  int64_t before = 0;
-  for (int base = 0; base < n; base += kPlanThreads) {
-    const int i = base + threadIdx.x;
-    const int v = i < n ? need[i] : 0;
-    int total;
-    const int end = block_scan<kPlanThreads>(v, s_warp, total);
-    if (i < n) need[i] = static_cast<int32_t>(min(before + end - v, static_cast<int64_t>(1) << 30));
-    before += total;
-  }
-  __syncthreads();
-  return static_cast<int>(min(before, static_cast<int64_t>(1) << 30));
+constexpr int kNear = 2048;  // page ids kept in shared memory; more go through the workspace
+
+// Runs of table entries to be dealt with, one per argument of a group: the
+// warps take them in turn, a lane an entry, so that the long rows of a few
+// sequences are spread over the CTA.  `count` < 1: none.
+struct Runs {
+  int64_t from[kPlanThreads], to[kPlanThreads];
+  int count[kPlanThreads];
+};
+template <typename F>
+__device__ __forceinline__ void each_run(const Runs& runs, int n, F act) {
+  for (int i = threadIdx.x >> 5; i < min(n, kPlanThreads); i += kPlanThreads / 32)
+    if (runs.count[i] > 0) act(runs.from[i], runs.to[i], runs.count[i]);
 }
+// Entries table[from + lane + 32 j], four loads at once.
+template <typename F>
+__device__ __forceinline__ void each_entry(const int32_t* table, int64_t from, int count, F act) {
+  for (int j = threadIdx.x & 31; j < count; j += 128) {
+    int id[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) id[u] = j + 32 * u < count ? table[from + j + 32 * u] : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (j + 32 * u < count) act(j + 32 * u, id[u]);
+  }
+}
+
+// The arguments are taken kPlanThreads at a time, a thread each.  Every value
+// that does not wait for the call's own changes (lengths, last pages, the
+// first chunk of counts) is read before the first barrier: the kernel's time
+// is the number of loads that have to follow one another.
 
 // Set the length of sequences seqs[i] to lens[i].
 //   1. pages past a shorter length are let go;
@@ -114,87 +134,143 @@ __device__ int sum_needs(int32_t* need, int n, int* s_warp) {
 __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const PagePool p, const int32_t* seqs, const int32_t* lens,
                                                               int n, PagesWs w, unsigned* status) {
   __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int32_t s_free[kNear];
   __shared__ int s_copies;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* before = w.need;
-  int32_t* flag = w.need + n;  // 0: nothing to do, 1: grows, 2: grows out of a shared page
+  __shared__ unsigned long long s_wanted;
+  __shared__ Runs runs;
   pdl_launch_dependents();
   pdl_wait();
-  if (threadIdx.x == 0) s_copies = 0;
-  // 1: a warp per sequence, a lane per page.
-  for (int i = warp; i < n; i += kPlanThreads / 32) {
-    const int s = seqs[i];
-    if (s < 0 || s >= p.n_seqs) {
-      if (lane == 0) raise_status(status, kStatusBadId);
-      continue;
-    }
-    const int len = p.kv_len[s], want = lens[i];
-    if (want < 0 || up(want, p.page_size) > p.max_pages || want > len) continue;
-    const int had = min(up(max(len, 0), p.page_size), p.max_pages), keep = up(want, p.page_size);
-    int32_t* row = p.table + static_cast<int64_t>(s) * p.max_pages;
-    for (int j = keep + lane; j < had; j += 32) {
-      const int id = row[j];
-      if (id >= 0 && id < p.n_pages)
-        atomicSub(p.refs + id, 1);
-      else
+  if (threadIdx.x == 0) s_copies = s_wanted = 0;
+  // 1
+  int s = -1, len = 0, want = 0, last = -1;  // of the last group of arguments: the only one, for up to kPlanThreads
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + static_cast<int>(threadIdx.x);
+    int keep = 0, had = 0;
+    s = last = -1;
+    if (i < n) {
+      s = seqs[i];
+      want = lens[i];
+      if (s < 0 || s >= p.n_seqs) {
         raise_status(status, kStatusBadId);
-      row[j] = -1;
-    }
-    if (lane == 0) p.kv_len[s] = want;
-  }
-  __syncthreads();
-  // 2
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int s = seqs[i];
-    int need = 0, f = 0;
-    if (s >= 0 && s < p.n_seqs) {
-      const int len = max(p.kv_len[s], 0), want = lens[i];
-      if (want < 0 || up(want, p.page_size) > p.max_pages) {
-        raise_status(status, kStatusNoPages);
-      } else if (want > len) {
-        const int had = up(len, p.page_size);
-        f = 1;
-        need = up(want, p.page_size) - had;
-        if (len % p.page_size != 0) {
-          const int id = p.table[static_cast<int64_t>(s) * p.max_pages + had - 1];
-          if (id >= 0 && id < p.n_pages && __ldcg(p.refs + id) > 1) {
-            f = 2;
-            ++need;
-          }
+        s = -1;
+      } else {
+        len = max(p.kv_len[s], 0);
+        had = up(len, p.page_size);
+        if (want < 0 || up(want, p.page_size) > p.max_pages || had > p.max_pages) {
+          raise_status(status, kStatusNoPages);
+          s = -1;
+          had = 0;
+        } else {
+          if (want > len && len % p.page_size != 0) last = p.table[static_cast<int64_t>(s) * p.max_pages + had - 1];
+          keep = min(had, up(want, p.page_size));
+          if (want <= len) p.kv_len[s] = want;
         }
       }
     }
-    before[i] = need;
-    flag[i] = f;
-  }
-  __syncthreads();
-  const int total = sum_needs(before, n, s_warp);
-  const int have = total ? find_free(p.refs, p.n_pages, min(total, p.n_pages), w.rank, s_warp) : 0;
-  // 4
-  for (int i = warp; i < n; i += kPlanThreads / 32) {
-    if (flag[i] == 0) continue;
-    const int s = seqs[i], len = max(p.kv_len[s], 0), want = lens[i];
-    const int had = up(len, p.page_size), shared = flag[i] == 2;
-    const int first = had - shared, upto = up(want, p.page_size), at = before[i];
-    if (at + (upto - first) > have) {
-      if (lane == 0) raise_status(status, kStatusNoPages);
-      continue;
+    runs.from[threadIdx.x] = static_cast<int64_t>(max(s, 0)) * p.max_pages + keep;
+    runs.count[threadIdx.x] = had - keep;
+    if (__syncthreads_or(keep < had)) {
+      each_run(runs, n - base, [&](int64_t from, int64_t, int count) {
+        each_entry(p.table, from, count, [&](int j, int id) {
+          if (id >= 0 && id < p.n_pages)
+            atomicSub(p.refs + id, 1);
+          else
+            raise_status(status, kStatusBadId);
+          p.table[from + j] = -1;
+        });
+      });
+      __syncthreads();
     }
-    int32_t* row = p.table + static_cast<int64_t>(s) * p.max_pages;
-    for (int j = first + lane; j < upto; j += 32) {
-      const int id = w.rank[at + j - first];
-      if (shared && j == first) {
-        const int k = atomicAdd(&s_copies, 1), old = row[j];
-        w.src[k] = old;
-        w.dst[k] = id;
-        atomicSub(p.refs + old, 1);
+  }
+  // 2 to 4
+  const int4 refs0 = load_refs(p.refs, p.n_pages, 0);
+  int64_t dealt = 0;
+  int found = 0;  // free pages found
+  int32_t* ids = s_free;
+  const bool one_group = n <= kPlanThreads;
+  if (!one_group) {
+    // One search finds the pages of all groups: as many as they may want.
+    unsigned long long wanted = 0;
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+      const int t = seqs[i];
+      if (t < 0 || t >= p.n_seqs) continue;
+      const int l = max(p.kv_len[t], 0), v = lens[i];
+      if (v > l && up(v, p.page_size) <= p.max_pages) wanted += up(v, p.page_size) - up(l, p.page_size) + 1;
+    }
+    atomicAdd(&s_wanted, wanted);
+    __syncthreads();
+    const int most = static_cast<int>(min(s_wanted, static_cast<unsigned long long>(p.n_pages)));
+    if (most > kNear) ids = w.rank;
+    if (most > 0) found = find_free(p.refs, p.n_pages, most, refs0, ids, s_warp);
+  }
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + static_cast<int>(threadIdx.x);
+    if (!one_group) {
+      s = last = -1;
+      if (i < n) {
+        s = seqs[i];
+        want = lens[i];
+        if (s < 0 || s >= p.n_seqs) {
+          s = -1;
+        } else {
+          len = max(p.kv_len[s], 0);
+          if (want < 0 || up(want, p.page_size) > p.max_pages || up(len, p.page_size) > p.max_pages) s = -1;
+          if (s >= 0 && want > len && len % p.page_size != 0)
+            last = p.table[static_cast<int64_t>(s) * p.max_pages + up(len, p.page_size) - 1];
+        }
       }
-      row[j] = id;
+    }
+    const bool grows = s >= 0 && want > len;
+    const bool shared = grows && last >= 0 && last < p.n_pages && __ldcg(p.refs + last) > 1;
+    const int first = up(len, p.page_size) - shared, need = grows ? up(want, p.page_size) - first : 0;
+    int total;
+    const int64_t at = dealt + block_scan<kPlanThreads>(need, s_warp, total) - need;
+    if (one_group && total > 0) {
+      if (total > kNear) ids = w.rank;
+      found = find_free(p.refs, p.n_pages, min(total, p.n_pages), refs0, ids, s_warp);
+    }
+    dealt += total;
+    const bool fits = grows && at + need <= found;
+    if (grows && !fits) raise_status(status, kStatusNoPages);
+    const int64_t row = static_cast<int64_t>(max(s, 0)) * p.max_pages + first;
+    if (fits) {
+      p.kv_len[s] = want;
+      if (shared) {
+        const int k = atomicAdd(&s_copies, 1);
+        w.src[k] = last;
+        w.dst[k] = ids[at];
+      }
+    }
+    // A shared page is let go when every group has looked at its count.
+    if (one_group) {
+      if (fits && shared) atomicSub(p.refs + last, 1);
+    } else if (i < n) {
+      w.left[i] = fits && shared ? last : -1;
+    }
+    // New pages: one by its thread, more by a warp.
+    const int gets = fits ? need : 0;
+    if (gets == 1) {
+      const int id = ids[at];
+      p.table[row] = id;
       p.refs[id] = 1;
     }
-    if (lane == 0) p.kv_len[s] = want;
+    runs.from[threadIdx.x] = at;
+    runs.to[threadIdx.x] = row;
+    runs.count[threadIdx.x] = gets > 1 ? gets : 0;
+    if (__syncthreads_or(gets > 1)) {
+      each_run(runs, n - base, [&](int64_t from, int64_t to, int count) {
+        for (int j = threadIdx.x & 31; j < count; j += 32) {
+          const int id = ids[from + j];
+          p.table[to + j] = id;
+          p.refs[id] = 1;
+        }
+      });
+      __syncthreads();
+    }
   }
   __syncthreads();
+  for (int i = threadIdx.x; !one_group && i < n; i += kPlanThreads)
+    if (w.left[i] >= 0) atomicSub(p.refs + w.left[i], 1);
   if (threadIdx.x == 0) w.count[0] = s_copies;
 }
 
@@ -203,62 +279,70 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const PagePool p, 
 __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const PagePool p, const int32_t* parents,
                                                             const int32_t* children, int n, PagesWs w, unsigned* status) {
   __shared__ int s_warp[kPlanThreads / 32];
+  __shared__ int32_t s_free[kNear];
   __shared__ int s_copies;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* before = w.need;
-  int32_t* flag = w.need + n;  // 1: a fork
+  __shared__ Runs runs;
   pdl_launch_dependents();
   pdl_wait();
   if (threadIdx.x == 0) s_copies = 0;
-  for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int s = parents[i], c = children[i];
-    int need = 0, f = 0;
-    if (s < 0 || s >= p.n_seqs || c < 0 || c >= p.n_seqs || p.kv_len[c] != 0) {
-      raise_status(status, kStatusBadId);
-    } else {
-      const int len = p.kv_len[s];
-      f = len > 0 && up(len, p.page_size) <= p.max_pages;
-      need = f && len % p.page_size != 0;
-    }
-    before[i] = need;
-    flag[i] = f;
-  }
-  __syncthreads();
-  const int total = sum_needs(before, n, s_warp);
-  const int have = total ? find_free(p.refs, p.n_pages, min(total, p.n_pages), w.rank, s_warp) : 0;
-  for (int i = warp; i < n; i += kPlanThreads / 32) {
-    if (flag[i] == 0) continue;
-    const int s = parents[i], c = children[i], len = p.kv_len[s];
-    const int full = len / p.page_size, part = len % p.page_size != 0, at = before[i];
-    if (at + part > have) {
-      if (lane == 0) raise_status(status, kStatusNoPages);
-      continue;
-    }
-    const int32_t* from = p.table + static_cast<int64_t>(s) * p.max_pages;
-    int32_t* to = p.table + static_cast<int64_t>(c) * p.max_pages;
-    for (int j = lane; j < full; j += 32) {
-      const int id = from[j];
-      to[j] = id;
-      if (id >= 0 && id < p.n_pages)
-        atomicAdd(p.refs + id, 1);
-      else
+  const int4 refs0 = load_refs(p.refs, p.n_pages, 0);
+  const int most = min(n, p.n_pages);  // a fork takes one page at most
+  int32_t* ids = most <= kNear ? s_free : w.rank;
+  const int have = find_free(p.refs, p.n_pages, most, refs0, ids, s_warp);
+  int dealt = 0;
+  for (int base = 0; base < n; base += kPlanThreads) {
+    const int i = base + static_cast<int>(threadIdx.x);
+    int s = -1, c = -1, len = 0;
+    if (i < n) {
+      s = parents[i];
+      c = children[i];
+      if (s < 0 || s >= p.n_seqs || c < 0 || c >= p.n_seqs || p.kv_len[c] != 0) {
         raise_status(status, kStatusBadId);
+        s = -1;
+      } else {
+        len = p.kv_len[s];
+        if (len <= 0 || up(len, p.page_size) > p.max_pages) s = -1;
+      }
     }
-    if (lane == 0) {
+    const int full = s >= 0 ? len / p.page_size : 0;
+    const bool part = s >= 0 && len % p.page_size != 0;
+    const int64_t from = static_cast<int64_t>(max(s, 0)) * p.max_pages, to = static_cast<int64_t>(max(c, 0)) * p.max_pages;
+    const int last = part ? p.table[from + full] : -1;
+    int total;
+    const int at = dealt + block_scan<kPlanThreads>(part, s_warp, total) - part;
+    const bool fits = at + part <= have;
+    if (s >= 0 && !fits) raise_status(status, kStatusNoPages);
+    const int gets = s >= 0 && fits ? full : 0;
+    if (s >= 0 && fits) {
+      p.kv_len[c] = len;
       if (part) {
-        const int id = w.rank[at], old = from[full];
-        if (old >= 0 && old < p.n_pages) {
+        const int id = ids[at];
+        if (last >= 0 && last < p.n_pages) {
           const int k = atomicAdd(&s_copies, 1);
-          w.src[k] = old;
+          w.src[k] = last;
           w.dst[k] = id;
         } else {
           raise_status(status, kStatusBadId);
         }
-        to[full] = id;
+        p.table[to + full] = id;
         p.refs[id] = 1;
       }
-      p.kv_len[c] = len;
     }
+    runs.from[threadIdx.x] = from;
+    runs.to[threadIdx.x] = to;
+    runs.count[threadIdx.x] = gets;
+    __syncthreads();
+    each_run(runs, n - base, [&](int64_t a, int64_t b, int count) {
+      each_entry(p.table, a, count, [&](int j, int id) {
+        p.table[b + j] = id;
+        if (id >= 0 && id < p.n_pages)
+          atomicAdd(p.refs + id, 1);
+        else
+          raise_status(status, kStatusBadId);
+      });
+    });
+    __syncthreads();
+    dealt += total;
   }
   __syncthreads();
   if (threadIdx.x == 0) w.count[0] = s_copies;
@@ -289,30 +373,53 @@ __global__ void __launch_bounds__(kPlanThreads) compact_count_kernel(const PageP
   if (threadIdx.x == 0) w.chunks[blockIdx.x] = total;
 }
 
+// Up to kOwnCount chunks every CTA counts all of them itself (the counts come
+// from L2, all loads at once), which is quicker than a kernel before this one;
+// a thread's part of a chunk is four bits.
+constexpr int kOwnCount = 16;
+
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagePool p, PagesWs w) {
   __shared__ int s_warp[kPlanThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  // Live pages in all, and in the chunks before this one and before L's.
-  const int chunks = gridDim.x, me = blockIdx.x;
-  const int v = threadIdx.x < chunks ? __ldcg(w.chunks + threadIdx.x) : 0;
-  int L, before_me, below, r[4], t;
-  (void)block_scan<kPlanThreads>(v, s_warp, L);
-  (void)block_scan<kPlanThreads>(static_cast<int>(threadIdx.x) < me ? v : 0, s_warp, before_me);
-  const int cl = L / kChunkPages;
-  (void)block_scan<kPlanThreads>(static_cast<int>(threadIdx.x) < cl ? v : 0, s_warp, below);
-  if (L % kChunkPages != 0) {
-    const int p0 = cl * kChunkPages + 4 * threadIdx.x;
-    (void)load_live4(p.refs, p.n_pages, p0, r);
-    int n = 0;
+  const int chunks = gridDim.x, me = blockIdx.x, tid = threadIdx.x;
+  int L, before_me, below, r[4], t;  // pages in use; those in chunks before this one; those below L
+  if (chunks <= kOwnCount) {
+    uint64_t bits = 0;
+#pragma unroll 4
+    for (int c = 0; c < chunks; ++c) {
+      (void)load_live4(p.refs, p.n_pages, c * kChunkPages + 4 * tid, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) n += p0 + i < L && r[i] > 0;
-    (void)block_scan<kPlanThreads>(n, s_warp, t);
-    below += t;
+      for (int i = 0; i < 4; ++i) bits |= static_cast<uint64_t>(r[i] > 0) << (4 * c + i);
+    }
+    (void)block_scan<kPlanThreads>(__popcll(bits), s_warp, L);
+    (void)block_scan<kPlanThreads>(__popcll(bits & ((1ull << (4 * me)) - 1)), s_warp, before_me);
+    const int cl = L / kChunkPages;  // L's chunk; past the last one when every page is in use
+    uint64_t low = ~0ull;
+    if (cl < kOwnCount) {
+      const int in = min(max(L - cl * kChunkPages - 4 * tid, 0), 4);
+      low = ((1ull << (4 * cl)) - 1) | (((1ull << in) - 1) << (4 * cl));
+    }
+    (void)block_scan<kPlanThreads>(__popcll(bits & low), s_warp, below);
+  } else {
+    const int v = tid < chunks ? __ldcg(w.chunks + tid) : 0;
+    (void)block_scan<kPlanThreads>(v, s_warp, L);
+    (void)block_scan<kPlanThreads>(tid < me ? v : 0, s_warp, before_me);
+    const int cl = L / kChunkPages;
+    (void)block_scan<kPlanThreads>(tid < cl ? v : 0, s_warp, below);
+    if (L % kChunkPages != 0) {
+      const int p0 = cl * kChunkPages + 4 * tid;
+      (void)load_live4(p.refs, p.n_pages, p0, r);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += p0 + i < L && r[i] > 0;
+      (void)block_scan<kPlanThreads>(n, s_warp, t);
+      below += t;
+    }
   }
-  const int p0 = me * kChunkPages + 4 * threadIdx.x;
+  const int p0 = me * kChunkPages + 4 * tid;
   const int live = load_live4(p.refs, p.n_pages, p0, r);
-  int rank = before_me + block_scan<kPlanThreads>(live, s_warp, t) - live;  // live pages before p0
+  int rank = before_me + block_scan<kPlanThreads>(live, s_warp, t) - live;  // pages in use before p0
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int id = p0 + i;
@@ -325,7 +432,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagePo
     }
     rank += r[i] > 0;
   }
-  if (me == 0 && threadIdx.x == 0) {
+  if (me == 0 && tid == 0) {
     w.count[0] = L - below;
     w.count[1] = L;
   }
@@ -438,7 +545,7 @@ int launch_pages_fork(const PagePool& p, const int32_t* parents, const int32_t* 
 int launch_pages_compact(const PagePool& p, void* ws, unsigned* status, cudaStream_t s) {
   const PagesWs w = split_ws(ws, p.n_pages);
   const int chunks = (p.n_pages + kChunkPages - 1) / kChunkPages;
-  if (!launch_pdl(compact_count_kernel, chunks, kPlanThreads, s, p, w)) return TQ1_ERR_CUDA;
+  if (chunks > kOwnCount && !launch_pdl(compact_count_kernel, chunks, kPlanThreads, s, p, w)) return TQ1_ERR_CUDA;
   if (!launch_pdl(compact_plan_kernel, chunks, kPlanThreads, s, p, w)) return TQ1_ERR_CUDA;
   return launch_list_copy(p, w, w.rank, status, s);
 }
