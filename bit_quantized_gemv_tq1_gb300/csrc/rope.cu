@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kMaxRotPairs = 128;  // head_dim <= 256
+constexpr int kPer = 2;            // tokens of a CTA, where there are many
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
@@ -46,17 +47,54 @@ __device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
   v[3] = b.y;
 }
 
-// One CTA: `per` tokens from blockIdx.x * per on, and of each token's items
-// (groups of 8 elements of the q, k and v heads) those of part blockIdx.y of
-// gridDim.y.
+// One CTA: `per` tokens from blockIdx.x * per on, and of each token's heads
+// (of q, k and v) the blockIdx.y-th part of gridDim.y.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache c, const KvBatch b, const RopeArgs a,
                                                                    int per, unsigned* status) {
-  __shared__ float2 s_cs[4][kMaxRotPairs];
-  __shared__ int s_seq[4], s_pos[4], s_page[4];
+  __shared__ float2 s_cs[kPer][kMaxRotPairs];
+  __shared__ int s_seq[kPer], s_pos[kPer], s_page[kPer];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tok0 = blockIdx.x * per;
+  // A thread keeps its group of 8 elements and walks the CTA's (token, head)
+  // pairs with a step and a compare.  One pair at a time and two tokens a
+  // CTA: what hides the loads is many resident threads, not many loads each
+  // (12 381 tokens of 40 + 2 x 8 heads of 128: 86 us, 6.2 TB/s; with two or
+  // four pairs held per thread 97 and 106 us, with four or eight tokens a CTA
+  // 90 and 92 us).
+  const int pairs = a.rot >> 1, groups = c.d >> 3, heads = a.n_q + 2 * c.n_kv;
+  const int h_lo = static_cast<int>(static_cast<int64_t>(heads) * blockIdx.y / gridDim.y);
+  const int h_n = static_cast<int>(static_cast<int64_t>(heads) * (blockIdx.y + 1) / gridDim.y) - h_lo;
+  const int stride = kRopeThreads / groups, grp = tid % groups;
+  const bool in_rot = grp < (a.rot >> 3), halves = in_rot && !a.interleaved;
+  // Elements e0 .. e0+3 and e1 .. e1+3 of the head; of v always 8 neighbours.
+  const int n0 = 8 * grp, n1 = n0 + 4, e0 = halves ? 4 * grp : n0, e1 = halves ? e0 + pairs : n1;
+  const int upto = tid < stride * groups ? min(per, b.t - tok0) : 0;  // tokens; threads past the last whole head idle
+  int w = 0, h = tid / groups;
+  auto settle = [&]() {
+    while (w < upto && h >= h_n) {
+      h -= h_n;
+      ++w;
+    }
+  };
+  settle();
+  float x[4], y[4];
+  int u = -1, head = 0;  // token and head of what x and y hold; token -1: nothing left
+  auto fetch = [&]() {
+    u = w < upto ? w : -1;
+    head = h_lo + h;
+    if (u < 0) return;
+    const bool is_q = head < a.n_q, is_v = head >= a.n_q + c.n_kv, turn = in_rot && !is_v;
+    const TI* src = static_cast<const TI*>(is_q ? a.q : is_v ? a.v : a.k) +
+                    static_cast<int64_t>(tok0 + u) * (is_q ? a.ldq : is_v ? a.ldv : a.ldk) +
+                    static_cast<int64_t>(is_q ? head : is_v ? head - a.n_q - c.n_kv : head - a.n_q) * c.d;
+    load4(src + (turn ? e0 : n0), x);
+    load4(src + (turn ? e1 : n1), y);
+    h += stride;
+    settle();
+  };
   pdl_wait();
+  fetch();  // on their way while the tokens' places are looked up
   // The sequence of each token, its position and its page: a warp per token.
   if (warp < per) {
     const int tok = tok0 + warp;
@@ -82,77 +120,54 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache
     }
   }
   __syncthreads();
-  const int pairs = a.rot >> 1;
   for (int i = tid; i < per * pairs; i += kRopeThreads) {
-    const int w = i / pairs, p = i - w * pairs;
-    if (s_seq[w] < 0) continue;
-    const int pos = a.positions ? __ldg(a.positions + tok0 + w) : s_pos[w];
+    const int t = i / pairs, p = i - t * pairs;
+    if (s_seq[t] < 0) continue;
+    const int pos = a.positions ? __ldg(a.positions + tok0 + t) : s_pos[t];
     double half_turns = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + p)) * 0.31830988618379067154;
     half_turns -= 2.0 * rint(0.5 * half_turns);
     float sn, cs;
     sincospif(static_cast<float>(half_turns), &sn, &cs);
-    s_cs[w][p] = make_float2(cs * a.mscale, sn * a.mscale);
+    s_cs[t][p] = make_float2(cs * a.mscale, sn * a.mscale);
   }
   __syncthreads();
-  const int groups = c.d >> 3, rotg = a.rot >> 3;
-  const int heads = a.n_q + 2 * c.n_kv;
-  const int items = heads * groups;
-  const int from = static_cast<int>(static_cast<int64_t>(items) * blockIdx.y / gridDim.y);
-  const int to = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.y + 1) / gridDim.y);
-  const int span = to - from;
-  for (int i = tid; i < per * span; i += kRopeThreads) {
-    const int w = i / span, item = from + i - w * span;
-    if (s_seq[w] < 0) continue;
-    const int tok = tok0 + w;
-    const int head = item / groups, grp = item - head * groups;
-    const bool is_q = head < a.n_q, is_v = head >= a.n_q + c.n_kv;
-    const TI* src;
+  for (; u >= 0; fetch()) {
+    const bool is_q = head < a.n_q, is_v = head >= a.n_q + c.n_kv, turn = in_rot && !is_v;
+    if (s_seq[u] < 0 || (!is_q && s_page[u] < 0)) continue;
     TO* dst;
-    if (is_q) {
-      src = static_cast<const TI*>(a.q) + tok * a.ldq + static_cast<int64_t>(head) * c.d;
-      dst = reinterpret_cast<TO*>(a.q_out) + (static_cast<int64_t>(tok) * a.n_q + head) * c.d;
-    } else {
-      if (s_page[w] < 0) continue;
-      const int h = is_v ? head - a.n_q - c.n_kv : head - a.n_q;
-      src = is_v ? static_cast<const TI*>(a.v) + tok * a.ldv : static_cast<const TI*>(a.k) + tok * a.ldk;
-      src += static_cast<int64_t>(h) * c.d;
-      dst = reinterpret_cast<TO*>(is_v ? c.v : c.k) + s_page[w] * c.page_stride + h * c.head_stride +
-            (s_pos[w] & (c.page_size - 1)) * c.slot_stride;
-    }
-    const bool turn = !is_v && grp < rotg;
-    // Elements e0 .. e0+3 and e1 .. e1+3 of the head.
-    const bool halves = turn && !a.interleaved;
-    const int e0 = halves ? 4 * grp : 8 * grp, e1 = halves ? e0 + pairs : e0 + 4;
-    float x[4], y[4];
-    load4(src + e0, x);
-    load4(src + e1, y);
-    if (halves) {
+    if (is_q)
+      dst = reinterpret_cast<TO*>(a.q_out) + (static_cast<int64_t>(tok0 + u) * a.n_q + head) * c.d;
+    else
+      dst = reinterpret_cast<TO*>(is_v ? c.v : c.k) + s_page[u] * c.page_stride +
+            (is_v ? head - a.n_q - c.n_kv : head - a.n_q) * c.head_stride + (s_pos[u] & (c.page_size - 1)) * c.slot_stride;
+    const float2* cs = s_cs[u];
+    if (turn && halves) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 cs = s_cs[w][e0 + j];
-        const float u = x[j] * cs.x - y[j] * cs.y;
-        y[j] = x[j] * cs.y + y[j] * cs.x;
-        x[j] = u;
+        const float2 t = cs[e0 + j];
+        const float v = x[j] * t.x - y[j] * t.y;
+        y[j] = x[j] * t.y + y[j] * t.x;
+        x[j] = v;
       }
     } else if (turn) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float2 c0 = s_cs[w][(e0 >> 1) + j], c1 = s_cs[w][(e1 >> 1) + j];
-        float u = x[2 * j] * c0.x - x[2 * j + 1] * c0.y;
-        x[2 * j + 1] = x[2 * j] * c0.y + x[2 * j + 1] * c0.x;
-        x[2 * j] = u;
-        u = y[2 * j] * c1.x - y[2 * j + 1] * c1.y;
-        y[2 * j + 1] = y[2 * j] * c1.y + y[2 * j + 1] * c1.x;
-        y[2 * j] = u;
+        const float2 t0 = cs[(e0 >> 1) + j], t1 = cs[(e1 >> 1) + j];
+        float v = x[2 * j] * t0.x - x[2 * j + 1] * t0.y;
+        x[2 * j + 1] = x[2 * j] * t0.y + x[2 * j + 1] * t0.x;
+        x[2 * j] = v;
+        v = y[2 * j] * t1.x - y[2 * j + 1] * t1.y;
+        y[2 * j + 1] = y[2 * j] * t1.y + y[2 * j + 1] * t1.x;
+        y[2 * j] = v;
       }
     }
     const uint2 lo = make_uint2(pack2<TO>(x[0], x[1]), pack2<TO>(x[2], x[3]));
     const uint2 hi = make_uint2(pack2<TO>(y[0], y[1]), pack2<TO>(y[2], y[3]));
-    if (halves) {
+    if (turn && halves) {
       *reinterpret_cast<uint2*>(dst + e0) = lo;
       *reinterpret_cast<uint2*>(dst + e1) = hi;
     } else {
-      *reinterpret_cast<uint4*>(dst + e0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      *reinterpret_cast<uint4*>(dst + n0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
   }
 }
@@ -178,12 +193,12 @@ __global__ void rope_freqs_kernel(float* inv_freq, int pairs, double base, doubl
 
 template <typename TI, typename TO>
 int launch(const KvCache& c, const KvBatch& b, const RopeArgs& a, unsigned* status, cudaStream_t s) {
-  // Four tokens a CTA share its start; while that leaves SMs without a CTA,
-  // one token a CTA, its items split over as many CTAs as keep one item a
-  // thread.
+  // Two tokens a CTA share its start; while that leaves SMs without a CTA,
+  // one token a CTA, its heads split over as many CTAs as leave a thread one
+  // group of 8 elements.
   const int items = (a.n_q + 2 * c.n_kv) * (c.d >> 3);
   const int sms = device_info().num_sms;
-  const int per = b.t >= 8 * sms ? 4 : 1;
+  const int per = b.t >= 8 * sms ? kPer : 1;
   const int64_t gx = (static_cast<int64_t>(b.t) + per - 1) / per;
   int gy = 1;
   while (gy < 16 && gx * gy < 2 * sms && items > gy * kRopeThreads) ++gy;
