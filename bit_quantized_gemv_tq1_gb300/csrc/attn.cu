@@ -28,10 +28,11 @@ namespace tq1 {
 namespace {
 
 constexpr int kAWarps = 8, kAThreads = 32 * kAWarps;
+constexpr int kAShift = 7;                // a block is 128 keys
 constexpr int kARows = 16;                // rows of a tile (one m16 operand)
 constexpr int kWarpKeys = 16;             // keys of a block per warp
 constexpr int kABlock = kWarpKeys * kAWarps;
-static_assert(kABlock == kBlockKeys, "a warp does 16 keys of every block");
+static_assert(kABlock == 1 << kAShift, "a warp does 16 keys of every block");
 
 template <int D>
 struct WarpCfg {
@@ -122,25 +123,6 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const int row0 = tile * kARows, rows = min(kARows, sq.n * plan.group - row0);
     const int pos0 = sq.len - sq.n;  // position of the sequence's first new token
 
-    // The tile's queries: fragments of a 16 x D operand, rows past the end zero.
-    uint32_t qf[D / 16][4];
-    int lo[2], hi[2];  // keys [lo, hi) that rows g and g + 8 see
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g + 8 * h;
-      const bool there = r < rows;
-      const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
-      const uint16_t* src = a.q + (sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks)) : 0u;
-        qf[ks][2 + h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8)) : 0u;
-      }
-      const int pos = pos0 + tok;
-      hi[h] = there ? (plan.causal ? min(sq.len, pos + 1) : sq.len) : 0;
-      lo[h] = plan.window ? max(0, pos - plan.window + 1) : 0;
-    }
-
     const int key0 = (fb + blk) * kABlock + warp * kWarpKeys;  // this warp's keys: key0, key0 + 128, ...
     const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
     const uint16_t *kbase = c.k + head * c.head_stride, *vbase = c.v + head * c.head_stride;
@@ -179,12 +161,32 @@ __global__ void __launch_bounds__(kAThreads, 1)
       cp_commit();
     };
 
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+
+    // The tile's queries: fragments of a 16 x D operand, rows past the end zero.
+    uint32_t qf[D / 16][4];
+    int lo[2], hi[2];  // keys [lo, hi) that rows g and g + 8 see
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      const bool there = r < rows;
+      const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
+      const uint16_t* src = a.q + (sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[ks][h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks)) : 0u;
+        qf[ks][2 + h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8)) : 0u;
+      }
+      const int pos = pos0 + tok;
+      hi[h] = there ? (plan.causal ? min(sq.len, pos + 1) : sq.len) : 0;
+      lo[h] = plan.window ? max(0, pos - plan.window + 1) : 0;
+    }
+
     float o[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
     for (int i = 0; i < todo; ++i) {
       issue(i + C::kStages - 1);
       cp_wait<C::kStages - 1>();
@@ -340,6 +342,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
   __shared__ float4 s_v[kJoinWarps][32];
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
   pdl_wait();
   const Part p0 = parts[2 * c], p1 = parts[2 * c + 1];
   const bool second = p1.rows > 0;  // a CTA begins at most one tile that it does not end, its last
@@ -379,8 +382,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 namespace {
 
-int attn_ctas() { return device_info().num_sms; }
-
 // Which kernel a call takes, by the rows (tokens x query heads of a kv head)
 // of an average sequence: kWarps for up to one 16-row tile, else the 128-row
 // kernel, with two such tiles side by side where one does not hold them.
@@ -389,6 +390,7 @@ Route route(int64_t t, int64_t group, int64_t n_seqs) {
   const int64_t rows = (t * group + n_seqs - 1) / n_seqs;
   return rows <= kARows ? kWarps : rows <= (128 / group) * group ? kTile : kTilePair;
 }
+int attn_ctas() { return device_info().num_sms; }  // both kernels: one per SM
 int route_rows(Route r, int group) { return r == kWarps ? kARows : attn_tile_rows(group, r == kTilePair); }
 
 template <typename Kernel, typename... Args>
@@ -419,7 +421,7 @@ int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, int ctas,
       return TQ1_ERR_CUDA;
     configured[di.device].store(true, std::memory_order_release);
   }
-  const TilePlan plan = {kARows, a.n_q / c.n_kv, a.causal, a.window};
+  const TilePlan plan = {kARows, a.n_q / c.n_kv, a.causal, a.window, kAShift};
   return launch_pdl(attn_warp_kernel<T, D>, dim3(ctas), kAThreads, C::kSmem, s, c, b, a, plan, parts, slots, status)
              ? TQ1_OK
              : TQ1_ERR_CUDA;
@@ -439,7 +441,7 @@ int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a,
   }
   if (rc != TQ1_OK) return rc;
   const int rows = route_rows(r, group);
-  const int share = std::min(8, (rows * (D / 4) + 31) / 32);  // at most 8 CTAs an SM: all resident at once
+  const int share = std::min(8, (rows * (D / 4) + 31) / 32);  // 8 CTAs an SM: all resident at once
   return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 32 * kJoinWarps, 0, s, a, rows, group,
                     static_cast<const Part*>(parts), static_cast<const float*>(slots))
              ? TQ1_OK
@@ -449,10 +451,9 @@ int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a,
 }  // namespace
 
 size_t attn_workspace_bytes(const KvCache& c, int64_t t, int64_t n_q, int64_t n_seqs) {
-  const int ctas = attn_ctas();
   const int group = static_cast<int>(n_q / c.n_kv);
   if (group < 1 || group > 128) return 0;
-  const int rows = max(kARows, route_rows(route(t, group, n_seqs), group));
+  const int ctas = attn_ctas(), rows = std::max(kARows, route_rows(route(t, group, n_seqs), group));
   const size_t b = join_parts_bytes(ctas) + 2 * static_cast<size_t>(ctas) * join_slot_floats(rows, c.d) * sizeof(float);
   return (b + 255) & ~size_t(255);
 }

@@ -51,7 +51,7 @@ constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // 
 // Registers per thread: 384 x 168 at launch = 2 x 128 x 208 + 128 x 88.
 constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
-constexpr int kTBlock = kBlockKeys;
+constexpr int kTShift = 7, kTBlock = 1 << kTShift;  // keys of a block
 constexpr float kMoveAt = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
 
 template <int D, bool PAIR>
@@ -774,7 +774,7 @@ int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool
   k.c = c;
   k.b = b;
   k.a = a;
-  k.plan = {attn_tile_rows(group, pair), group, a.causal, a.window};
+  k.plan = {attn_tile_rows(group, pair), group, a.causal, a.window, kTShift};
   k.parts = parts;
   k.slots = slots;
   k.status = status;

@@ -66,9 +66,9 @@ __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
 // [W c / C, W (c+1) / C) of the W in the list.  So every CTA has the same
 // work to one unit whatever the sequences' lengths are, and only the tiles at
 // a CTA's two ends are shared: their parts are joined afterwards.
-constexpr int kBlockKeys = 128;
 struct TilePlan {
   int rows, group, causal, window;
+  int shift;  // log2 of a block's keys
 };
 
 // Blocks of one tile: the first one and how many.  A tile whose rows see
@@ -79,8 +79,8 @@ __device__ __forceinline__ void tile_blocks(const TilePlan& p, const Seq& s, int
   const int pos0 = s.len - s.n + tok0, pos1 = s.len - s.n + tok1;
   const int hi = p.causal ? min(s.len, pos1 + 1) : s.len;
   const int lo = p.window ? max(0, pos0 - p.window + 1) : 0;
-  first = lo / kBlockKeys;
-  count = max(1, (hi + kBlockKeys - 1) / kBlockKeys - first);
+  first = lo >> p.shift;
+  count = max(1, ((hi + (1 << p.shift) - 1) >> p.shift) - first);
   if (hi <= lo) count = 1;
 }
 __device__ __forceinline__ int seq_tiles(const TilePlan& p, const Seq& s) {
