@@ -47,7 +47,7 @@ namespace tq1 {
 
 namespace {
 
-constexpr int kTThreads = 384, kMmaWarp = 8, kLoadWarp = 9, kPlanWarp = 10;  // warp 11 makes the third warp group whole
+constexpr int kTThreads = 384, kMmaWarp = 0, kLoadWarp = 1, kPlanWarp = 2;  // warp 11 makes the third warp group whole
 // Registers per thread: 384 x 168 at launch = 2 x 128 x 208 + 128 x 88.
 constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
@@ -97,12 +97,34 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return wait_or_abort(bar, parity, abort_flag);
+// A wait that ends in any case and says nothing: the phase completed, or
+// another role has aborted, or ~2 s went by, in which case it sets the flag
+// itself.  Whoever goes on after an abort works on what is there; the call
+// reports TQ1_ERR_TIMEOUT.  One block of instructions to the compiler, which
+// sees no branch in it.
+__device__ __forceinline__ void wait_soft(uint64_t* bar, uint32_t parity, int* abort_flag) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u64 t, t0;\n\t.reg .u32 f;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t0, %%globaltimer;\n\t"
+      "add.u64 t0, t0, %3;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared.u32 f, [%2];\n\t"
+      "setp.ne.u32 q, f, 0;\n\t"
+      "@q bra DONE;\n\t"
+      "mov.u64 t, %%globaltimer;\n\t"
+      "setp.lt.u64 q, t, t0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "st.volatile.shared.u32 [%2], 1;\n\t"
+      "DONE:\n\t}" ::"r"(smem_addr(bar)),
+      "r"(parity), "r"(smem_addr(abort_flag)), "l"(kWaitLimitNs)
+      : "memory");
 }
+// The value of lane 0, which the compiler then knows to be every lane's.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Keys by elements (K order down the rows, 64 elements of N along a row):
 // the operand's N-major order, 128-byte swizzle.  Blocks of 64 elements lie
@@ -264,18 +286,10 @@ __global__ void __launch_bounds__(kTThreads, 1)
     return true;
   };
 
-  auto next_segment_one = [&]() {
-    const uint32_t i = seg_at % kSegs;
-    if (!wait_one(&seg_full[i], (seg_at / kSegs) & 1u, abort_flag)) return false;
-    g = s_seg[i];
-    mbar_arrive(&seg_empty[i]);
-    ++seg_at;
-    return true;
-  };
-  if (warp < kMmaWarp) {
+  if (warp >= 4) {
     // ---------------------------------------------------------- weights --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
-    const int s = warp >> 2, row = tid & (kTRows - 1);
+    const int s = (warp >> 2) - 1, row = tid & (kTRows - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t st_at = tmem + lanes + C::kS + 128 * s, o_at = tmem + lanes + C::kO + s * D;
     const float sc = k.a.scale * kLog2e;
@@ -462,7 +476,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           out[trow] = mrow;
           out[((k.plan.rows + 3) & ~3) + trow] = lrow;
         }
-        if (tid == 0 && g.starts) k.parts[slot] = Part{g.head, g.q0, g.tok0 * k.plan.group, g.rows, g.last_cta, {}};
+        if (tid == 128 && g.starts) k.parts[slot] = Part{g.head, g.q0, g.tok0 * k.plan.group, g.rows, g.last_cta, {}};
       }
       if (!PAIR) {
         // The other stream has read this one's O and s_ml before either goes on.
@@ -481,107 +495,111 @@ __global__ void __launch_bounds__(kTThreads, 1)
       // In a step (a block's second product and the first product kStep
       // blocks on) the streams take turns; issued from a warp each, their
       // instructions would interleave and both streams' products finish late
-      // (670 us where this order takes 560: 4096 tokens on 12288 keys, 40/8
-      // heads of 128).  The whole warp walks the loop and one lane issues:
-      // what the instructions take (descriptors, addresses) is then the same
-      // in all lanes to the compiler too, which keeps it in uniform registers
-      // instead of moving it there before each of them (700 us).
+      // (4096 tokens on 12288 keys, 40/8 heads of 128: 670 us for 560).
+      //
+      // The whole warp walks the loop without a branch on what a lane has
+      // seen (wait_soft), and one lane issues: addresses and descriptors are
+      // then the same in all lanes to the compiler too, which keeps them in
+      // the uniform registers that the instructions take.
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
       constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
-      constexpr bool lead = true;
-      if (elect_one()) {
+      const bool lead = elect_one();
       const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
       const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
       uint32_t pph = 0, qph = 0;   // phases of p_full (a bit per stream) and q_full
       uint32_t tph = 0;            // and of each slot's tail (a bit per slot)
-      bool ok = true;
-      auto product_s = [&](int s, uint32_t slot) {
-        const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
-        if (lead) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
-            umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
-          }
-          umma_commit(&s_full[s]);
-        }
-      };
-      auto product_o = [&](int s, uint32_t slot, int steps, uint32_t keep) {
-        const uint32_t s_col = tmem + C::kS + 128 * s, o_col = tmem + C::kO + s * D;
-        const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
-        if (lead) {
-          if (steps == kTBlock / 16) {
-#pragma unroll
-            for (int ks = 0; ks < kTBlock / 16; ++ks)
-              umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
-          } else {
-            for (int ks = 0; ks < steps; ++ks)
-              umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
-          }
-        }
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (lead) umma_commit(bar);
-      };
-      uint32_t ri = 0, rph = 0;
+      uint32_t ri = 0, rph = 0;    // ring slot to be consumed next, its phase
       auto step = [&]() {
         if (++ri == C::kRing) {
           ri = 0;
           rph ^= 1u;
         }
       };
-      while (ok && next_segment_one() && g.todo > 0) {
-        if (g.empty) continue;
-        const int n = g.todo;
-        if (!(ok = wait_one(&q_full, qph, abort_flag))) break;
+      auto product_s = [&](int s, uint32_t slot) {
+        const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
+          umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[s]);
+      };
+      auto product_o = [&](int s, uint32_t slot, int steps, uint32_t keep) {
+        const uint32_t s_col = tmem + C::kS + 128 * s, o_col = tmem + C::kO + s * D;
+        const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
+        if (steps == kTBlock / 16) {
+#pragma unroll
+          for (int ks = 0; ks < kTBlock / 16; ++ks)
+            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
+        } else {
+          for (int ks = 0; ks < steps; ++ks)
+            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
+        }
+      };
+      for (uint32_t at = 0;; ++at) {
+        wait_soft(&seg_full[at % kSegs], (at / kSegs) & 1u, &s_abort);
+        const int n = uniform(*abort_flag ? 0 : s_seg[at % kSegs].todo), none = uniform(s_seg[at % kSegs].empty);
+        const int first_key = uniform(s_seg[at % kSegs].first_key), hi = uniform(s_seg[at % kSegs].hi);
+        const int len = uniform(s_seg[at % kSegs].len);
+        if (lead) mbar_arrive(&seg_empty[at % kSegs]);
+        if (n == 0) break;
+        if (none) continue;
+        wait_soft(&q_full, qph, &s_abort);
         qph ^= 1u;
-        for (int i = 0; i < C::kStep && i < n; ++i) {
-          if (!(ok = wait_one(&full[ri], rph, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < C::kStep; ++i) {
+          if (i >= n) break;
+          wait_soft(&full[ri], rph, &s_abort);
           tc_fence_after();
-          product_s(PAIR ? 0 : i, ri);
-          if (PAIR) product_s(1, ri);
-          commit(&empty[ri]);
+          if (lead) {
+            product_s(PAIR ? 0 : i, ri);
+            if (PAIR) product_s(1, ri);
+            umma_commit(&empty[ri]);
+          }
           step();
         }
-        for (int i = 0; ok && i < n; ++i) {
+        for (int i = 0; i < n; ++i) {
           const bool more = i + C::kStep < n;
-          if (i + C::kStep == n || (i == 0 && n < C::kStep)) commit(&q_empty);  // the last first product is on its way
-          const int key0 = g.first_key + i * kTBlock;
-          const int steps = (min(kTBlock, g.hi - key0) + 15) >> 4;
+          // The last first product is on its way.
+          if (lead && (i + C::kStep == n || (i == 0 && n < C::kStep))) umma_commit(&q_empty);
+          const int key0 = first_key + i * kTBlock;
+          const int steps = (min(kTBlock, hi - key0) + 15) >> 4;
           const uint32_t slot = ri, sph = rph;
           step();
           const uint32_t nslot = ri, nph = rph;
           if (more) step();
-          if (g.len - key0 < 16 * steps) {  // what lies past the end is zeroed first
-            ok = wait_one(&tail[slot], (tph >> slot) & 1u, abort_flag);
+          if (len - key0 < 16 * steps) {  // what lies past the end is zeroed first
+            wait_soft(&tail[slot], (tph >> slot) & 1u, &s_abort);
             tph ^= 1u << slot;
           } else {
-            ok = wait_one(&full[slot], sph, abort_flag);
+            wait_soft(&full[slot], sph, &s_abort);
           }
-          if (ok && more) ok = wait_one(&full[nslot], nph, abort_flag);
+          if (more) wait_soft(&full[nslot], nph, &s_abort);
 #pragma unroll
           for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
             const int s = PAIR ? u : (i & 1);
-            if (!ok || !(ok = wait_one(&p_full[s], (pph >> s) & 1u, abort_flag))) break;
+            wait_soft(&p_full[s], (pph >> s) & 1u, &s_abort);
             pph ^= 1u << s;
             tc_fence_after();
-            product_o(s, slot, steps, i >= C::kStep ? 1u : 0u);
-            if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
-            if (more) {
-              product_s(s, nslot);
-              if (u == (PAIR ? 1 : 0)) umma_commit(&empty[nslot]);
-            } else {
-              umma_commit(&o_full[s]);
+            if (lead) {
+              product_o(s, slot, steps, i >= C::kStep ? 1u : 0u);
+              if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
+              if (more) {
+                product_s(s, nslot);
+                if (u == (PAIR ? 1 : 0)) umma_commit(&empty[nslot]);
+              } else {
+                umma_commit(&o_full[s]);
+              }
             }
           }
         }
       }
       // After an abort, let the products already issued finish (bounded).
+      __syncwarp();
       if (*abort_flag) {
-        commit(&drained);
+        if (lead) umma_commit(&drained);
         (void)mbar_wait(&drained, 0);
-      }
       }
     } else if (warp == kLoadWarp) {
       // --------------------------------------------------------- copies --
