@@ -26,13 +26,13 @@
 // with it, through registers) only when a row's maximum has grown by more than
 // 2^8 over it; weights up to 2^8 lose nothing, 16-bit floats being relative.
 //
-// Roles: warps 0-3 and 4-7 the two streams' weights (a thread a row), warp 8
-// the matrix instructions, warp 9 the copies (TMA, a box per page and 64
-// elements, 128-byte swizzle), warp 10 walks the CTA's tiles for all of them.
+// Roles: warp 0 the matrix instructions, warp 1 the copies (TMA, a box per
+// page and 64 elements, 128-byte swizzle), warp 2 walks the CTA's tiles for all
+// of them, warps 4-7 and 8-11 the two streams' weights (a thread a row).
 // Keys at or past a sequence's length are not read at all where a whole page
-// of them is, and otherwise warp 10 overwrites their values with zeros in
-// shared memory before the second product: a weight of zero would not silence
-// a NaN there.
+// of them is, and otherwise their values are overwritten with zeros in shared
+// memory before the second product: a weight of zero would not silence a NaN
+// there.
 //
 // Every wait is bounded; the first that runs out sets an abort flag that
 // releases the others, and TQ1_ERR_TIMEOUT is raised.
@@ -47,7 +47,7 @@ namespace tq1 {
 
 namespace {
 
-constexpr int kTThreads = 384, kMmaWarp = 0, kLoadWarp = 1, kPlanWarp = 2;  // warp 11 makes the third warp group whole
+constexpr int kTThreads = 384, kMmaWarp = 0, kLoadWarp = 1, kPlanWarp = 2;  // warp 3 makes the first warp group whole
 // Registers per thread: 384 x 168 at launch = 2 x 128 x 208 + 128 x 88.
 constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
                      const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using C = TileCfg<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing], tail[C::kRing];
+  __shared__ __align__(8) uint64_t full[C::kRing], empty[C::kRing];
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], swap, drained;
   __shared__ __align__(8) uint64_t seg_full[kSegs], seg_empty[kSegs];
   __shared__ Segment s_seg[kSegs];
@@ -240,7 +240,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&tail[i], 1);
     }
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
@@ -295,6 +294,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const float sc = k.a.scale * kLog2e;
     uint32_t done = 0;   // blocks this stream has done, over all segments
     uint32_t oph = 0;    // phase of o_full
+    uint32_t base_slot = 0;  // ring slots of the segments before
     uint32_t swaps = 0;  // phases of `swap` passed
     bool ok = true;
     // This thread's row: its place in every tile (whole tokens, so its token
@@ -392,6 +392,22 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
+          // The values past the sequence's end, up to the end of the last 16
+          // that are multiplied, are zeroed by the first stream that reads
+          // them.  They are the segment's last ring slot, whose use before
+          // this one was over before this S began, and this one is not
+          // without p_full: the phase waited for is the only one it can be.
+          const int from = g.len - key0, upto = (min(kTBlock, g.hi - key0) + 15) & ~15;
+          if (from < upto && (!PAIR || s == 0)) {
+            const uint32_t at = base_slot + 2 * g.todo - 1, slot = at % C::kRing;
+            if (!(ok = wait_all(&full[slot], (at / C::kRing) & 1u, abort_flag))) break;
+            for (int e = row; e < (upto - from) * (D / 8); e += kTRows) {
+              const int r = from + e / (D / 8), c = e % (D / 8);
+              *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
@@ -399,6 +415,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           ++done;
         }
         if (!ok) break;
+        base_slot += 2 * g.todo;
       }
       const bool mine = !g.empty && (PAIR || s < g.todo);  // this stream's O holds something
       if (mine) {
@@ -508,7 +525,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
       const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
       uint32_t pph = 0, qph = 0;   // phases of p_full (a bit per stream) and q_full
-      uint32_t tph = 0;            // and of each slot's tail (a bit per slot)
       uint32_t ri = 0, rph = 0;    // ring slot to be consumed next, its phase
       auto step = [&]() {
         if (++ri == C::kRing) {
@@ -541,7 +557,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         wait_soft(&seg_full[at % kSegs], (at / kSegs) & 1u, &s_abort);
         const int n = uniform(*abort_flag ? 0 : s_seg[at % kSegs].todo), none = uniform(s_seg[at % kSegs].empty);
         const int first_key = uniform(s_seg[at % kSegs].first_key), hi = uniform(s_seg[at % kSegs].hi);
-        const int len = uniform(s_seg[at % kSegs].len);
         if (lead) mbar_arrive(&seg_empty[at % kSegs]);
         if (n == 0) break;
         if (none) continue;
@@ -569,12 +584,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           step();
           const uint32_t nslot = ri, nph = rph;
           if (more) step();
-          if (len - key0 < 16 * steps) {  // what lies past the end is zeroed first
-            wait_soft(&tail[slot], (tph >> slot) & 1u, &s_abort);
-            tph ^= 1u << slot;
-          } else {
-            wait_soft(&full[slot], sph, &s_abort);
-          }
+          wait_soft(&full[slot], sph, &s_abort);
           if (more) wait_soft(&full[nslot], nph, &s_abort);
 #pragma unroll
           for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
@@ -661,14 +671,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         if (segs) (void)mbar_wait(&q_full, (segs - 1) & 1u);
       }
     } else if (warp == kPlanWarp) {
-      // ------------------------------------------------- plan and tails --
-      // Hands out the segments, one ahead of the one whose tail it tends:
-      // zeros over the values past a sequence's end, up to the end of the
-      // last group of 16 that is multiplied.  A segment's last values are its
-      // last ring slot.  A barrier per slot: the slot is not filled again
-      // before its products are done, so no phase can be missed.
-      Segment last = {};
-      uint32_t slots_done = 0;
+      // ----------------------------------------------------------- plan --
       int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
       int64_t left = st.units, unit = st.first;
       Seq sq = st.sq;
@@ -710,23 +713,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
             blk = 0;
           }
         }
-        if (last.todo > 0 && !last.empty) {
-          const uint32_t at = slots_done + 2 * last.todo - 1, slot = at % C::kRing;
-          slots_done += 2 * last.todo;
-          const int key0 = last.first_key + (last.todo - 1) * kTBlock;
-          const int upto = (min(kTBlock, last.hi - key0) + 15) & ~15, from = last.len - key0;
-          if (from < upto) {
-            if (!wait_all(&full[slot], (at / C::kRing) & 1u, abort_flag)) break;
-            for (int r = from; r < upto; ++r)
-              for (int c = lane; c < (D / 64) * 8; c += 32)
-                *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 +
-                                          (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tail[slot]);
-          }
-        }
-        last = g;
       }
     }
   }

@@ -71,14 +71,16 @@ def attention(b, q, scale, causal, window):
       sums       n terms of fp32"""
     t, n_q, d = q.shape
     group, u, tiny = n_q // b.n_kv, UNIT[b.dtype], TINY[b.dtype]
-    out, tol = torch.zeros(t, n_q, d, dtype=torch.float64), torch.zeros(t, n_q, d, dtype=torch.float64)
+    where = "cuda" if torch.cuda.is_available() else "cpu"  # fp64 either way
+    out, tol = (torch.zeros(t, n_q, d, dtype=torch.float64, device=where) for _ in range(2))
+    q = q.to(where)
     at = 0
     for i, (n, ln) in enumerate(zip(b.new, b.len)):
         if n and ln:
-            k, v = b.sequence(i, 0), b.sequence(i, 1)
-            pos = torch.arange(ln - n, ln)[:, None]
-            j = torch.arange(ln)[None, :]
-            seen = torch.ones(n, ln, dtype=torch.bool)
+            k, v = b.sequence(i, 0).to(where), b.sequence(i, 1).to(where)
+            pos = torch.arange(ln - n, ln, device=where)[:, None]
+            j = torch.arange(ln, device=where)[None, :]
+            seen = torch.ones(n, ln, dtype=torch.bool, device=where)
             if causal:
                 seen &= j <= pos
             if window:
@@ -98,7 +100,7 @@ def attention(b, q, scale, causal, window):
                 tol[at:at + n, h] = ((u + 4 * dx + 2.0 ** -20 + 2 * ln * 2.0 ** -24) * a
                                      + ln * tiny * v[:, h // group].abs().amax() / l)
         at += n
-    return out, tol
+    return out.cpu(), tol.cpu()
 
 
 def rounded(tol, ref, dtype):

@@ -111,6 +111,27 @@ def test_large_scores(new, dtype):
     check(b, 4, scale=1.0)
 
 
+@pytest.mark.parametrize("d,n_kv,group,window,dtype", [(64, 8, 3, 1024, F16), (64, 8, 4, 0, BF16), (128, 8, 5, 0, BF16),
+                                                       (128, 4, 3, 700, F16), (128, 8, 1, 0, F16)])
+@pytest.mark.parametrize("new", [[45, 11, 6, 1062, 1463, 1, 539, 82], [30, 60, 17, 5, 41, 90, 33, 77, 2, 64]])
+def test_many_blocks_and_tiles_for_every_cta(d, n_kv, group, window, dtype, new):
+    # Every CTA has many blocks of several tiles, most sequences end inside a
+    # group of 16 keys, and what lies past their ends is NaN.
+    ctx = [935, 535, 960, 2224, 2409, 2508, 1289, 187, 3001, 4444]
+    check(Batch(new, [a + b for a, b in zip(new, ctx)], 32, n_kv, d, dtype, seed=d + group, junk=float("nan")), n_kv * group,
+          window=window)
+
+
+@pytest.mark.parametrize("new", [1, 12, 400])
+def test_large_scores_in_long_runs(new):
+    # The running maximum moves in the middle of a CTA's run of blocks.
+    b = Batch([new] * 3, [new + 4000, new + 3111, new + 5003], 64, 8, 64, F16, seed=new)
+    for i, ln in enumerate(b.len):
+        for j, p in enumerate(b.table[i, :-(-ln // 64)].long().tolist()):
+            b.kv[0, p] = (b.kv[0, p].float() * (0.2 + 0.1 * j)).to(F16)
+    check(b, 16, scale=0.5)
+
+
 def test_fp32_output_feeds_the_quantiser():
     check(Batch([1, 100], [200, 300], 16, 2, 128, BF16), 8, f32=True)
 
