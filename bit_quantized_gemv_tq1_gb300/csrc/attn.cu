@@ -39,9 +39,11 @@ struct WarpCfg {
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr uint32_t kTile = kWarpKeys * D * 2;           // one warp's keys (or values) of a block
   static constexpr uint32_t kRing = kAWarps * kStages * 2 * kTile;
-  static constexpr uint32_t kSmem = kRing;
-  // The joining of the warps overlays the ring.
-  static_assert(kAWarps * kARows * (D + 2) * 4 <= kRing, "join buffer");
+  // Behind the ring, for the joining of the warps: m and l of all their rows,
+  // O of eight rows at a time.
+  static constexpr uint32_t kJoin = kAWarps * (2 * kARows + 8 * D) * 4;
+  static constexpr uint32_t kSmem = kRing + kJoin;
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
@@ -94,11 +96,23 @@ __device__ __forceinline__ float quad_sum(float v) {
 
 }  // namespace
 
+namespace {
+
+// A tile's share of this CTA.
+struct WarpTile {
+  int head, seq, tile, blk, nb, todo;  // blocks [blk, blk + todo) of the tile's nb
+  int key0;                            // this warp's keys: key0, key0 + 128, ...
+  Seq sq;
+};
+
+}  // namespace
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kAThreads, 1)
     attn_warp_kernel(const KvCache c, const KvBatch b, const AttnArgs a, const TilePlan plan, Part* parts, float* slots,
                      unsigned* status) {
   using C = WarpCfg<D>;
+  constexpr int kAhead = C::kStages - 1;  // steps requested before the one being done
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, ctas = gridDim.x;
@@ -112,87 +126,119 @@ __global__ void __launch_bounds__(kAThreads, 1)
   __syncthreads();
 
   const uint32_t ring = smem_addr(smem) + warp * C::kStages * 2 * C::kTile;
+  float* const jm = reinterpret_cast<float*>(smem + C::kRing);
+  float* const jl = jm + kAWarps * kARows;
+  float* const jo = jl + kAWarps * kARows;
   const float sc = a.scale * kLog2e;
-  int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
-  Seq sq = st.sq;
-  int64_t left = st.units, unit = st.first;  // unit: of block blk
-  for (bool first_seg = true;; first_seg = false) {
-    int fb, nb;
-    tile_blocks(plan, sq, tile, fb, nb);
-    const int todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
-    const int row0 = tile * kARows, rows = min(kARows, sq.n * plan.group - row0);
-    const int pos0 = sq.len - sq.n;  // position of the sequence's first new token
 
-    const int key0 = (fb + blk) * kABlock + warp * kWarpKeys;  // this warp's keys: key0, key0 + 128, ...
-    const int32_t* table = b.table + static_cast<int64_t>(seq) * b.max_pages;
-    const uint16_t *kbase = c.k + head * c.head_stride, *vbase = c.v + head * c.head_stride;
-    int ids = -1;  // lane i: the page of step (32 n + i), for the steps being issued
-    // Request this warp's keys and values of step i; what lies past the
-    // sequence's end, or in no page, arrives as zeros.
-    auto issue = [&](int i) {
-      if (i < todo) {
-        if ((i & 31) == 0) {
-          const int k = key0 + (i + lane) * kABlock;
-          ids = -1;
-          if (i + lane < todo && k < sq.len) {
-            ids = __ldg(table + (k >> c.page_shift));
-            if (ids < 0 || ids >= c.n_pages) {
-              ids = -1;
-              raise_status(status, kStatusBadId);
-            }
-          }
-        }
-        const int k = key0 + i * kABlock;
-        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int64_t off = static_cast<int64_t>(max(page, 0)) * c.page_stride + (k & (c.page_size - 1)) * c.slot_stride;
-        const int have = page < 0 ? 0 : min(kWarpKeys, sq.len - k);
-        const uint32_t dst = ring + (i % C::kStages) * 2 * C::kTile;
-        constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+  auto open = [&](WarpTile& t, int64_t left) {
+    int fb;
+    tile_blocks(plan, t.sq, t.tile, fb, t.nb);
+    t.todo = static_cast<int>(min(static_cast<int64_t>(t.nb - t.blk), left));
+    t.key0 = (fb + t.blk) * kABlock + warp * kWarpKeys;
+  };
+  // Lane i: the page of step i0 + i of a tile, -1 where there is none.
+  auto pages_of = [&](const WarpTile& t, int i0) {
+    const int k = t.key0 + (i0 + lane) * kABlock;
+    if (i0 + lane >= t.todo || k >= t.sq.len) return -1;
+    const int id = __ldg(b.table + static_cast<int64_t>(t.seq) * b.max_pages + (k >> c.page_shift));
+    if (id >= 0 && id < c.n_pages) return id;
+    raise_status(status, kStatusBadId);
+    return -1;
+  };
+  // Request this warp's keys and values of step i into ring slot `slot`; what
+  // lies past the sequence's end, or in no page, arrives as zeros.
+  auto request = [&](const WarpTile& t, int ids, int i, uint32_t slot) {
+    const int k = t.key0 + i * kABlock;
+    const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+    const int64_t off = static_cast<int64_t>(max(page, 0)) * c.page_stride + t.head * c.head_stride +
+                        (k & (c.page_size - 1)) * c.slot_stride;
+    const int have = page < 0 ? 0 : min(kWarpKeys, t.sq.len - k);
+    const uint32_t dst = ring + slot * 2 * C::kTile;
+    constexpr int kChunks = D / 8;  // 16-byte pieces of a row
 #pragma unroll
-        for (int n = 0; n < kWarpKeys * kChunks / 32; ++n) {
-          const int p = n * 32 + lane, row = p / kChunks, ch = p % kChunks;
-          const bool there = row < have;
-          const int64_t at = off + (there ? row : 0) * c.slot_stride + ch * 8;
-          const uint32_t to = dst + row * D * 2 + ((ch ^ (row & 7)) << 4);
-          cp_async16(to, there ? kbase + at : c.k, there);
-          cp_async16(to + C::kTile, there ? vbase + at : c.v, there);
-        }
-      }
-      cp_commit();
-    };
+    for (int n = 0; n < kWarpKeys * kChunks / 32; ++n) {
+      const int p = n * 32 + lane, row = p / kChunks, ch = p % kChunks;
+      const bool there = row < have;
+      const int64_t at = off + row * c.slot_stride + ch * 8;
+      const uint32_t to = dst + row * D * 2 + ((ch ^ (row & 7)) << 4);
+      cp_async16(to, there ? c.k + at : c.k, there);
+      cp_async16(to + C::kTile, there ? c.v + at : c.v, there);
+    }
+  };
 
+  WarpTile cur = {st.head, st.seq, st.tile, st.block, 0, 0, 0, st.sq}, nxt = cur;
+  int64_t left = st.units, unit = st.first;  // unit: of cur's first block
+  open(cur, left);
+  int ids = pages_of(cur, 0), after = pages_of(cur, 32);  // of the 32 steps being requested, and of the 32 after them
+  uint32_t base = 0;                                      // ring slot of cur's step 0
+  auto slot_of = [&](int i) { return (base + static_cast<uint32_t>(i)) % C::kStages; };
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kAhead; ++i) {
+    if (i < cur.todo) request(cur, ids, i, slot_of(i));
+    cp_commit();
+  }
 
-    // The tile's queries: fragments of a 16 x D operand, rows past the end zero.
-    uint32_t qf[D / 16][4];
-    int lo[2], hi[2];  // keys [lo, hi) that rows g and g + 8 see
+  // A tile's queries: fragments of a 16 x D operand, rows past the end zero;
+  // and the keys [lo, hi) that rows g and g + 8 see.
+  uint32_t qf[D / 16][4];
+  int lo[2], hi[2];
+  auto load_queries = [&](const WarpTile& t) {
+    const int row0 = t.tile * kARows, rows = t.sq.n * plan.group - row0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = g + 8 * h;
       const bool there = r < rows;
-      const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
-      const uint16_t* src = a.q + (sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
+      const int tok = (row0 + r) / plan.group, qh = t.head * plan.group + (row0 + r) - tok * plan.group;
+      const uint16_t* src = a.q + (t.sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         qf[ks][h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks)) : 0u;
         qf[ks][2 + h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8)) : 0u;
       }
-      const int pos = pos0 + tok;
-      hi[h] = there ? (plan.causal ? min(sq.len, pos + 1) : sq.len) : 0;
+      const int pos = t.sq.len - t.sq.n + tok;
+      hi[h] = there ? (plan.causal ? min(t.sq.len, pos + 1) : t.sq.len) : 0;
       lo[h] = plan.window ? max(0, pos - plan.window + 1) : 0;
     }
+  };
+  load_queries(cur);
+
+  for (bool first_seg = true;; first_seg = false) {
+    // The next tile and its first pages are looked up now, and its first
+    // steps requested behind cur's last: the copies go on while the warps are
+    // joined (without this a CTA stood still for some 3 us per tile, of which
+    // a batch of 64 sequences has 3.4 a CTA).
+    const bool more = left > cur.todo;
+    int ids_n = -1;
+    if (more) {
+      nxt = cur;
+      next_tile(plan, b, nxt.head, nxt.seq, nxt.tile, nxt.sq);
+      nxt.blk = 0;
+      open(nxt, left - cur.todo);
+      ids_n = pages_of(nxt, 0);
+    }
+    const bool flows = more && cur.todo >= kAhead && nxt.todo >= kAhead;
 
     float o[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    for (int i = 0; i < todo; ++i) {
-      issue(i + C::kStages - 1);
-      cp_wait<C::kStages - 1>();
+    for (int i = 0; i < cur.todo; ++i) {
+      const int ask = i + kAhead;
+      if (ask < cur.todo) {
+        if ((ask & 31) == 0) {
+          ids = after;
+          after = pages_of(cur, ask + 32);
+        }
+        request(cur, ids, ask, slot_of(ask));
+      } else if (flows) {
+        request(nxt, ids_n, ask - cur.todo, slot_of(ask));
+      }
+      cp_commit();
+      cp_wait<kAhead>();
       __syncwarp();
-      const int k = key0 + i * kABlock;
-      const uint32_t kt = ring + (i % C::kStages) * 2 * C::kTile, vt = kt + C::kTile;
+      const int k = cur.key0 + i * kABlock;
+      const uint32_t kt = ring + slot_of(i) * 2 * C::kTile, vt = kt + C::kTile;
       float s[2][4] = {};
       {
         // Matrices of a K load: keys 0-7 / 8-15 by elements 0-7 / 8-15 of the step.
@@ -216,11 +262,11 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         const float mx = quad_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
         const float mn = fmaxf(m[h], mx);
-        const float base = mn == -INFINITY ? 0.0f : mn;  // no key seen yet: every weight below is exp2(-inf) = 0
-        const float keep = exp2f(m[h] - base);
+        const float base_m = mn == -INFINITY ? 0.0f : mn;  // no key seen yet: every weight below is exp2(-inf) = 0
+        const float keep = exp2f(m[h] - base_m);
         m[h] = mn;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = exp2f(x[j] - base);
+        for (int j = 0; j < 4; ++j) x[j] = exp2f(x[j] - base_m);
         l[h] = l[h] * keep + ((x[0] + x[1]) + (x[2] + x[3]));
         // The weights enter the second product as 16-bit numbers in [0, 1]
         // (the type the matrix instruction pairs with V's); the sum stays fp32.
@@ -248,67 +294,76 @@ __global__ void __launch_bounds__(kAThreads, 1)
       }
       __syncwarp();  // the slot is refilled by the next step's copies
     }
-    cp_wait<0>();
-    __syncthreads();
 
-    // Join the warps: every warp's m, l and O, then one thread per four
-    // elements of a row, warps in order.
-    float* jm = reinterpret_cast<float*>(smem);
-    float* jl = jm + kAWarps * kARows;
-    float* jo = jl + kAWarps * kARows;
+    // Join the warps, eight rows at a time: every warp's m, l and O, then one
+    // thread per four elements of a row, warps in order.
+    const int row0 = cur.tile * kARows, rows = min(kARows, cur.sq.n * plan.group - row0);
+    const bool whole = cur.blk == 0 && cur.todo == cur.nb;
+    const int slot = first_seg ? 2 * cta : 2 * cta + 1;
+    float* out = slots + slot * join_slot_floats(kARows, D);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      if (8 * h >= rows) break;
       const float lsum = quad_sum(l[h]);
-      const int r = g + 8 * h;
       if (qd == 0) {
-        jm[warp * kARows + r] = m[h];
-        jl[warp * kARows + r] = lsum;
+        jm[warp * kARows + 8 * h + g] = m[h];
+        jl[warp * kARows + 8 * h + g] = lsum;
       }
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float2*>(jo + (warp * kARows + r) * D + 8 * n + 2 * qd) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-    }
-    __syncthreads();
-    const bool whole = blk == 0 && todo == nb;
-    const int slot = first_seg ? 2 * cta : 2 * cta + 1;
-    float* out = slots + slot * join_slot_floats(kARows, D);
-    for (int e = tid; e < rows * (D / 4); e += kAThreads) {
-      const int r = e / (D / 4), col = (e % (D / 4)) * 4;
-      float mx = -INFINITY;
+        *reinterpret_cast<float2*>(jo + (warp * 8 + g) * D + 8 * n + 2 * qd) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+      __syncthreads();
+      for (int e = tid; e < min(8, rows - 8 * h) * (D / 4); e += kAThreads) {
+        const int rj = e / (D / 4), r = 8 * h + rj, col = (e % (D / 4)) * 4;
+        float mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kAWarps; ++w) mx = fmaxf(mx, jm[w * kARows + r]);
-      const float base = mx == -INFINITY ? 0.0f : mx;
-      float lt = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < kAWarps; ++w) mx = fmaxf(mx, jm[w * kARows + r]);
+        const float base_m = mx == -INFINITY ? 0.0f : mx;
+        float lt = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kAWarps; ++w) {
-        const float f = exp2f(jm[w * kARows + r] - base);
-        lt += f * jl[w * kARows + r];
-        const float4 x = *reinterpret_cast<const float4*>(jo + (w * kARows + r) * D + col);
-        v.x += f * x.x;
-        v.y += f * x.y;
-        v.z += f * x.z;
-        v.w += f * x.w;
-      }
-      if (whole) {
-        const float inv = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);  // a row that sees nothing is zero
-        const int tok = (row0 + r) / plan.group, qh = head * plan.group + (row0 + r) - tok * plan.group;
-        store4<T>(a, sq.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-      } else {
-        if (col == 0) {
-          out[r] = mx;
-          out[kARows + r] = lt;
+        for (int w = 0; w < kAWarps; ++w) {
+          const float f = exp2f(jm[w * kARows + r] - base_m);
+          lt += f * jl[w * kARows + r];
+          const float4 x = *reinterpret_cast<const float4*>(jo + (w * 8 + rj) * D + col);
+          v.x += f * x.x;
+          v.y += f * x.y;
+          v.z += f * x.z;
+          v.w += f * x.w;
         }
-        *reinterpret_cast<float4*>(out + slot_o(kARows, r, col)) = v;
+        if (whole) {
+          const float inv = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);  // a row that sees nothing is zero
+          const int tok = (row0 + r) / plan.group, qh = cur.head * plan.group + (row0 + r) - tok * plan.group;
+          store4<T>(a, cur.sq.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        } else {
+          if (col == 0) {
+            out[r] = mx;
+            out[kARows + r] = lt;
+          }
+          *reinterpret_cast<float4*>(out + slot_o(kARows, r, col)) = v;
+        }
+      }
+      __syncthreads();
+    }
+    if (!whole && cur.blk == 0 && tid == 0)
+      parts[slot] = Part{cur.head, cur.sq.q0, row0, rows, share_of(st.work, st.used, unit + cur.nb - 1), {}};
+    if (!more) break;
+    left -= cur.todo;
+    unit += cur.todo;
+    base += cur.todo;
+    cur = nxt;
+    ids = ids_n;
+    after = pages_of(cur, 32);
+    load_queries(cur);
+    if (!flows) {
+      cp_wait<0>();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (i < cur.todo) request(cur, ids, i, slot_of(i));
+        cp_commit();
       }
     }
-    if (!whole && blk == 0 && tid == 0) parts[slot] = Part{head, sq.q0, row0, rows, share_of(st.work, st.used, unit + nb - 1), {}};
-    left -= todo;
-    unit += todo;
-    if (left == 0) break;
-    __syncthreads();
-    next_tile(plan, b, head, seq, tile, sq);
-    blk = 0;
   }
 }
 
