@@ -102,6 +102,7 @@ namespace {
 struct WarpTile {
   int head, seq, tile, blk, nb, todo;  // blocks [blk, blk + todo) of the tile's nb
   int key0;                            // this warp's keys: key0, key0 + 128, ...
+  int lo, hi;                          // keys that some row sees
   Seq sq;
 };
 
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   const int g = lane >> 2, qd = lane & 3;
   pdl_wait();
   pdl_launch_dependents();
-  const Start st = find_start<kAThreads>(plan, b, c.n_kv, cta, ctas, reinterpret_cast<int*>(smem));
+  const Start st = find_start<kAThreads>(plan, b, c.n_kv, cta, ctas, reinterpret_cast<int64_t*>(smem));
   __syncthreads();
   if (tid < 2) parts[2 * cta + tid].rows = 0;
   if (st.units == 0) return;
@@ -136,30 +137,34 @@ __global__ void __launch_bounds__(kAThreads, 1)
     tile_blocks(plan, t.sq, t.tile, fb, t.nb);
     t.todo = static_cast<int>(min(static_cast<int64_t>(t.nb - t.blk), left));
     t.key0 = (fb + t.blk) * kABlock + warp * kWarpKeys;
+    const int row0 = t.tile * kARows, end = min(row0 + kARows, t.sq.n * plan.group), before = t.sq.len - t.sq.n;
+    t.lo = plan.window ? max(0, before + row0 / plan.group - plan.window + 1) : 0;
+    t.hi = plan.causal ? min(t.sq.len, before + (end - 1) / plan.group + 1) : t.sq.len;
   };
   // Lane i: the page of step i0 + i of a tile, -1 where there is none.
   auto pages_of = [&](const WarpTile& t, int i0) {
     const int k = t.key0 + (i0 + lane) * kABlock;
-    if (i0 + lane >= t.todo || k >= t.sq.len) return -1;
+    if (i0 + lane >= t.todo || k >= t.hi || k + kWarpKeys <= t.lo) return -1;
     const int id = __ldg(b.table + static_cast<int64_t>(t.seq) * b.max_pages + (k >> c.page_shift));
     if (id >= 0 && id < c.n_pages) return id;
     raise_status(status, kStatusBadId);
     return -1;
   };
   // Request this warp's keys and values of step i into ring slot `slot`; what
-  // lies past the sequence's end, or in no page, arrives as zeros.
+  // no row of the tile sees, or lies in no page, is not read and arrives as
+  // zeros (a weight of zero would not silence a NaN there).
   auto request = [&](const WarpTile& t, int ids, int i, uint32_t slot) {
     const int k = t.key0 + i * kABlock;
     const int page = __shfl_sync(0xffffffffu, ids, i & 31);
     const int64_t off = static_cast<int64_t>(max(page, 0)) * c.page_stride + t.head * c.head_stride +
                         (k & (c.page_size - 1)) * c.slot_stride;
-    const int have = page < 0 ? 0 : min(kWarpKeys, t.sq.len - k);
+    const int first = t.lo - k, have = page < 0 ? 0 : t.hi - k;
     const uint32_t dst = ring + slot * 2 * C::kTile;
     constexpr int kChunks = D / 8;  // 16-byte pieces of a row
 #pragma unroll
     for (int n = 0; n < kWarpKeys * kChunks / 32; ++n) {
       const int p = n * 32 + lane, row = p / kChunks, ch = p % kChunks;
-      const bool there = row < have;
+      const bool there = row >= first && row < have;
       const int64_t at = off + row * c.slot_stride + ch * 8;
       const uint32_t to = dst + row * D * 2 + ((ch ^ (row & 7)) << 4);
       cp_async16(to, there ? c.k + at : c.k, there);
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
   };
 
-  WarpTile cur = {st.head, st.seq, st.tile, st.block, 0, 0, 0, st.sq}, nxt = cur;
+  WarpTile cur = {st.head, st.seq, st.tile, st.block, 0, 0, 0, 0, 0, st.sq}, nxt = cur;
   int64_t left = st.units, unit = st.first;  // unit: of cur's first block
   open(cur, left);
   int ids = pages_of(cur, 0), after = pages_of(cur, 32);  // of the 32 steps being requested, and of the 32 after them

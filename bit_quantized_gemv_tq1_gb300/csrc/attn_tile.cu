@@ -30,9 +30,9 @@
 // page and 64 elements, 128-byte swizzle), warp 2 walks the CTA's tiles for all
 // of them, warps 4-7 and 8-11 the two streams' weights (a thread a row).
 // Keys at or past a sequence's length are not read at all where a whole page
-// of them is, and otherwise their values are overwritten with zeros in shared
-// memory before the second product: a weight of zero would not silence a NaN
-// there.
+// of them is; values that no token of the call sees are overwritten with
+// zeros in shared memory before the second product: a weight of zero would not
+// silence a NaN there.
 //
 // Every wait is bounded; the first that runs out sets an abort flag that
 // releases the others, and TQ1_ERR_TIMEOUT is raised.
@@ -66,7 +66,6 @@ struct TileCfg {
   // their values, so a segment of n blocks fills its ring slots in the order
   //   PAIR: K0 V0 K1 V1 K2 ...      else: K0 K1 V0 K2 V1 K3 V2 ...
   static constexpr int kStep = PAIR ? 1 : 2;
-  static __device__ __forceinline__ uint32_t key_slot(int i) { return PAIR ? 2 * i : (i ? 2 * i - 1 : 0); }
   static __device__ __forceinline__ uint32_t value_slot(int i, int n) { return PAIR ? 2 * i + 1 : i + min(i + 2, n); }
   static constexpr uint32_t kS = 0, kO = 256;  // tensor-memory columns: S of stream s at 128 s, O at kO + s D
 };
@@ -203,6 +202,7 @@ struct Segment {
   int pos0;                // position of its first token
   int tok0, rows;          // first token and rows of the tile
   int first_key, todo;     // blocks of the tile done here (0: no more segments)
+  int lo;                  // first key that some token of the sequence's sees
   int hi;                  // keys [.., hi) are seen by some row
   int starts, ends;        // whether they include the tile's first, last block
   int empty;               // no row sees a key: nothing is read
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   constexpr uint32_t tmem = 0;  // all 512 columns were asked for: they begin at column 0
   pdl_wait();
   pdl_launch_dependents();
-  const Start st = find_start<kTThreads>(k.plan, k.b, k.c.n_kv, cta, ctas, reinterpret_cast<int*>(sm));
+  const Start st = find_start<kTThreads>(k.plan, k.b, k.c.n_kv, cta, ctas, reinterpret_cast<int64_t*>(sm));
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies below write where the search wrote
   __syncthreads();
   if (tid < 2) k.parts[2 * cta + tid].rows = 0;
@@ -392,20 +392,25 @@ __global__ void __launch_bounds__(kTThreads, 1)
           }
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
-          // The values past the sequence's end, up to the end of the last 16
-          // that are multiplied, are zeroed by the first stream that reads
-          // them.  They are the segment's last ring slot, whose use before
-          // this one was over before this S began, and this one is not
-          // without p_full: the phase waited for is the only one it can be.
-          const int from = g.len - key0, upto = (min(kTBlock, g.hi - key0) + 15) & ~15;
-          if (from < upto && (!PAIR || s == 0)) {
-            const uint32_t at = base_slot + 2 * g.todo - 1, slot = at % C::kRing;
+          // Values that no token of the call sees (before the window of the
+          // sequence's first, or past its end, within the first and the last
+          // 16 that are multiplied) are zeroed by the first stream that reads
+          // them.  Their ring slot's use before this one was over before this
+          // S began, and this one is not without p_full: the phase waited for
+          // is the only one it can be.
+          const int below = g.lo - key0, from = g.len - key0, upto = (min(kTBlock, g.hi - key0) + 15) & ~15;
+          if ((below > 0 || from < upto) && (!PAIR || s == 0)) {
+            const uint32_t at = base_slot + C::value_slot(i, g.todo), slot = at % C::kRing;
             if (!(ok = wait_all(&full[slot], (at / C::kRing) & 1u, abort_flag))) break;
-            for (int e = row; e < (upto - from) * (D / 8); e += kTRows) {
-              const int r = from + e / (D / 8), c = e % (D / 8);
-              *reinterpret_cast<uint4*>(sm + (ring_at - sbase) + slot * C::kTile + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
+            uint8_t* const values = sm + (ring_at - sbase) + slot * C::kTile;
+            auto zero = [&](int r0, int r1) {
+              for (int e = row; e < (r1 - r0) * (D / 8); e += kTRows) {
+                const int r = r0 + e / (D / 8), c = e % (D / 8);
+                *reinterpret_cast<uint4*>(values + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+            };
+            if (below > 0) zero(below & ~15, below);
+            if (from < upto) zero(from, upto);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -541,22 +546,24 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         umma_commit(&s_full[s]);
       };
-      auto product_o = [&](int s, uint32_t slot, int steps, uint32_t keep) {
+      // Keys in steps of 16, [from, steps) of them.
+      auto product_o = [&](int s, uint32_t slot, int from, int steps, uint32_t keep) {
         const uint32_t s_col = tmem + C::kS + 128 * s, o_col = tmem + C::kO + s * D;
         const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
-        if (steps == kTBlock / 16) {
+        if (from == 0 && steps == kTBlock / 16) {
 #pragma unroll
           for (int ks = 0; ks < kTBlock / 16; ++ks)
             umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
         } else {
-          for (int ks = 0; ks < steps; ++ks)
-            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
+          for (int ks = from; ks < steps; ++ks)
+            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > from ? 1u : keep);
         }
       };
       for (uint32_t at = 0;; ++at) {
         wait_soft(&seg_full[at % kSegs], (at / kSegs) & 1u, &s_abort);
         const int n = uniform(*abort_flag ? 0 : s_seg[at % kSegs].todo), none = uniform(s_seg[at % kSegs].empty);
         const int first_key = uniform(s_seg[at % kSegs].first_key), hi = uniform(s_seg[at % kSegs].hi);
+        const int lo = uniform(s_seg[at % kSegs].lo);
         if (lead) mbar_arrive(&seg_empty[at % kSegs]);
         if (n == 0) break;
         if (none) continue;
@@ -579,7 +586,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           // The last first product is on its way.
           if (lead && (i + C::kStep == n || (i == 0 && n < C::kStep))) umma_commit(&q_empty);
           const int key0 = first_key + i * kTBlock;
-          const int steps = (min(kTBlock, hi - key0) + 15) >> 4;
+          const int steps = (min(kTBlock, hi - key0) + 15) >> 4, from = max(0, lo - key0) >> 4;
           const uint32_t slot = ri, sph = rph;
           step();
           const uint32_t nslot = ri, nph = rph;
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
             pph ^= 1u << s;
             tc_fence_after();
             if (lead) {
-              product_o(s, slot, steps, i >= C::kStep ? 1u : 0u);
+              product_o(s, slot, from, steps, i >= C::kStep ? 1u : 0u);
               if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
               if (more) {
                 product_s(s, nslot);
@@ -693,6 +700,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           g.todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
           const int end = row0 + g.rows;
           g.hi = k.plan.causal ? min(sq.len, g.pos0 + (end - 1) / k.plan.group + 1) : sq.len;
+          g.lo = k.plan.window ? max(0, g.pos0 - k.plan.window + 1) : 0;
           g.empty = g.hi <= (k.plan.window ? max(0, g.pos0 + g.tok0 - k.plan.window + 1) : 0);
           g.starts = blk == 0;
           g.ends = blk + g.todo == nb;

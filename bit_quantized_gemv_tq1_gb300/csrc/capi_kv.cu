@@ -167,7 +167,7 @@ int tq1_paged_attn(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const v
   if (n_q <= 0 || n_q % c.n_kv != 0 || window < 0 || !(scale > 0) || !std::isfinite(scale) || ldq < n_q * c.d ||
       ldo < n_q * c.d)
     return TQ1_ERR_SHAPE;
-  if ((c.d != 64 && c.d != 128) || n_q / c.n_kv > 128) return TQ1_ERR_UNSUPPORTED;
+  if ((c.d != 64 && c.d != 128) || n_q / c.n_kv > 128 || t * (n_q / c.n_kv) > (int64_t{1} << 30)) return TQ1_ERR_UNSUPPORTED;
   if (t == 0) return TQ1_OK;
   if (!q || !out || !ws) return TQ1_ERR_NULL;
   if (off16(q) || off16(out) || off16(ws) || ldq % 8 != 0 || ldo % 8 != 0) return TQ1_ERR_ALIGN;

@@ -88,11 +88,12 @@ __device__ __forceinline__ int seq_tiles(const TilePlan& p, const Seq& s) {
 }
 
 // Inclusive sum over a warp's lanes.
-__device__ __forceinline__ int warp_scan(int v) {
+template <typename I>
+__device__ __forceinline__ I warp_scan(I v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    const I u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -142,12 +143,12 @@ __device__ __forceinline__ int share_of(int64_t work, int used, int64_t u) {
 }
 
 // Called by all NT threads; every warp has the result.  `s_nb`: at least
-// n_seqs ints of shared memory, still read by other warps when the call
+// n_seqs words of shared memory, still read by other warps when the call
 // returns.  One barrier: the search stands before anything else of the call,
 // and of a small call it was the larger part (a form with a block-wide sum per
 // step took 5 us of the 70 us of a ragged batch of prompt chunks).
 template <int NT>
-__device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int* s_nb) {
+__device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int64_t* s_nb) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Blocks of each sequence: by its thread where it has one tile, else (left
   // as -1) by a warp, a lane per tile.
@@ -167,23 +168,23 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       const int t = s0 + __ffs(more) - 1;
       const Seq q = load_seq(b, t);
       const int tiles = seq_tiles(p, q);
-      int sum = 0;
+      int64_t sum = 0;
       for (int i = lane; i < tiles; i += 32) {
         int f, c;
         tile_blocks(p, q, i, f, c);
         sum += c;
       }
-      sum = __reduce_add_sync(0xffffffffu, sum);
-      if (lane == 0) s_nb[t] = sum;
+      sum = warp_scan(sum);
+      if (lane == 31) s_nb[t] = sum;
     }
   }
   __syncthreads();
   // A lane per run of sequences: their sum, the sum of all, and the lane
   // whose run holds the first unit.
   const int run = (b.n_seqs + 31) >> 5, s0 = lane * run, s1 = min(s0 + run, b.n_seqs);
-  int mine = 0;
+  int64_t mine = 0;
   for (int s = s0; s < s1; ++s) mine += s_nb[s];
-  const int end = warp_scan(mine);
+  const int64_t end = warp_scan(mine);
   const int64_t all = __shfl_sync(0xffffffffu, end, 31);  // blocks of one kv head
   Start r;
   const int64_t work = all * n_kv;
@@ -198,10 +199,10 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   r.first = share_begin(work, used, cta);
   r.units = share_begin(work, used, cta + 1) - r.first;
   r.head = work < (int64_t{1} << 31) ? static_cast<uint32_t>(r.first) / static_cast<uint32_t>(all) : static_cast<int>(r.first / all);
-  int rem = static_cast<int>(r.first - r.head * all);
+  int64_t rem = r.first - r.head * all;
   const int owner = __ffs(__ballot_sync(0xffffffffu, rem < end)) - 1;
   int seq = s0;
-  int into = rem - (end - mine);
+  int64_t into = rem - (end - mine);
   if (lane == owner)
     while (into >= s_nb[seq]) into -= s_nb[seq++];
   r.seq = __shfl_sync(0xffffffffu, seq, owner);
@@ -209,7 +210,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   const Seq q = load_seq(b, r.seq);
   r.sq = q;
   const int tiles = seq_tiles(p, q);
-  r.block = rem;
+  r.block = static_cast<int>(rem);
   for (int base = 0; tiles > 1 && base < tiles; base += 32) {
     int f, c = 0;
     if (base + lane < tiles) tile_blocks(p, q, base + lane, f, c);
@@ -217,7 +218,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
     if (rem < sum) {
       const int hit = __ffs(__ballot_sync(0xffffffffu, rem < upto)) - 1;
       r.tile = base + hit;
-      r.block = rem - __shfl_sync(0xffffffffu, upto - c, hit);
+      r.block = static_cast<int>(rem) - __shfl_sync(0xffffffffu, upto - c, hit);
       break;
     }
     rem -= sum;

@@ -519,11 +519,14 @@ size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64
  *      (TQ1_ERR_WORKSPACE otherwise), in use until the call's kernels finish
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights p
  * enter the second product as 16-bit numbers of the cache's type.  Slots at
- * or past kv_len may hold anything, NaN included; a value that is not finite
- * in a slot below kv_len reaches every row of the tiles that read it.
+ * or past kv_len, and slots before the window of a sequence's first new token,
+ * may hold anything, NaN included.  Keys that are not finite hurt only the
+ * rows that see them; values that are not finite, in a chunk of several
+ * tokens, also rows of nearby tokens that do not see them (a weight of zero
+ * does not silence them).
  * Deterministic.  head_dim 64 or 128, n_q a multiple of n_kv, at most 128
- * query heads per kv head (TQ1_ERR_UNSUPPORTED otherwise); scale > 0;
- * ldq, ldo multiples of 8.
+ * query heads per kv head, t * n_q / n_kv <= 2^30 (TQ1_ERR_UNSUPPORTED
+ * otherwise); scale > 0; ldq, ldo multiples of 8.
  * No passage: a convention of this library.
  */
 int tq1_paged_attn(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const void* q, int64_t ldq, int64_t t,

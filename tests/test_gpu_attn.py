@@ -86,6 +86,40 @@ def test_slots_past_the_end_may_hold_anything(junk, new):
     check(Batch([new, 1, new], [new + 3, 77, new + 130], 64, 2, 128, F16, junk=junk), 6)
 
 
+@pytest.mark.parametrize("window", [1, 5, 16, 100, 333])
+@pytest.mark.parametrize("new", [1, 3, 60])
+def test_what_a_window_leaves_out_may_hold_anything(window, new):
+    # Every slot before the window of a sequence's first new token holds NaN;
+    # one of the three has one token whatever the others have.
+    new = [new, 1, new]
+    length = [a + b for a, b in zip(new, (399, 128, 516))]
+    b = Batch(new, length, 16, 2, 64, F16, seed=window)
+    for i, (n, ln) in enumerate(zip(new, length)):
+        for j in range(max(0, ln - n + 1 - window)):
+            b.kv[:, b.table[i, j // 16], :, j % 16] = float("nan")
+    ref = Batch(new, length, 16, 2, 64, F16, seed=window)
+    b.to_gpu(lib())
+    q, gq = queries(b, 6)
+    out = run(b, gq, 6, window=window)
+    want, tol = attention(ref, q, 1 / 8, True, window)
+    assert ((out.cpu().double() - want).abs() <= rounded(tol, want, F16)).all()
+
+
+@pytest.mark.parametrize("new", [40, 300])
+def test_keys_that_are_not_finite_hurt_only_rows_that_see_them(new):
+    b = Batch([new], [new + 150], 16, 2, 64, F16)
+    clean = b.kv.clone()
+    bad = new + 150 - 7  # seen by the last seven tokens
+    b.kv[0, b.table[0, bad // 16], :, bad % 16] = float("nan")
+    b.to_gpu(lib())
+    q, gq = queries(b, 4)
+    out = run(b, gq, 4).cpu().double()
+    b.kv = clean
+    want, tol = attention(b, q, 1 / 8, True, 0)
+    tol = rounded(tol, want, F16)
+    assert ((out - want).abs() <= tol)[:-7].all() and out[-7:].isnan().all()
+
+
 @pytest.mark.parametrize("f32", [False, True])
 def test_rows_that_see_nothing_are_zero(f32):
     # More new tokens than the cache holds: the first rows stand before the

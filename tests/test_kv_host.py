@@ -69,7 +69,7 @@ def test_batches(lib, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(t=-1), SHAPE), (dict(t=(1 << 24) + 1), UNSUPPORTED), (dict(n_q=0), SHAPE), (dict(n_q=7), SHAPE), (dict(n_q=258, ldq=1 << 20, ldo=1 << 20), UNSUPPORTED),
     (dict(n_q=1 << 40), UNSUPPORTED), (dict(ldq=504), SHAPE), (dict(ldo=504), SHAPE), (dict(ldq=516), ALIGN), (dict(ldo=516), ALIGN),
-    (dict(window=-1), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("nan")), SHAPE),
+    (dict(t=1 << 24, n_q=256, ldq=1 << 20, ldo=1 << 20), UNSUPPORTED), (dict(window=-1), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("nan")), SHAPE),
     (dict(scale=float("inf")), SHAPE), (dict(q=None), NULL), (dict(out=None), NULL), (dict(ws=None), NULL),
     (dict(q=FAKE + 8), ALIGN), (dict(out=FAKE + 8), ALIGN), (dict(ws=FAKE + 8), ALIGN), (dict(t=0), 0),
 ])
