@@ -28,8 +28,8 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kChunkPages = 4 * kPlanThreads;  // pages of one compaction chunk
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;                                    // 16-byte pieces per thread and step
-constexpr int kCopyBytes = kCopyThreads * kCopyVecs * 16;       // bytes of one step of a CTA
+constexpr int kCopyVecs = 8;                             // 16-byte pieces per thread and step
+constexpr int kStepVecs = kCopyThreads * kCopyVecs;      // of one step of a CTA
 
 // Workspace: a header of 64 words, the copy list, and per-page / per-argument
 // scratch.
@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagePo
 }
 
 // ---------------------------------------------------------------- copies --
-// Every page of the list in every pool, in steps of kCopyBytes dealt to the
-// CTAs in order; and, after a compaction plan, the tables' and counts'
+// Every page of the list in every pool, in steps of 32 KB dealt to the CTAs in
+// order; and, after a compaction plan, the tables' and counts'
 // renaming, which touches nothing that is copied.
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagePool p, const int32_t* count, int64_t n_fixed,
                                                                   const int32_t* src, const int32_t* dst,
@@ -464,29 +464,53 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagePool
       p.refs[from] = 0;
     }
   }
-  const int steps = static_cast<int>((p.page_bytes + kCopyBytes - 1) / kCopyBytes);  // of one page
-  const int64_t all = n * p.n_pools * steps;
+  // A step of a CTA is 32 KB of one page, or as many whole pages as that
+  // holds: every thread has kCopyVecs loads in flight either way, and the
+  // grid can be small (two CTAs an SM), which is what an empty list costs.
+  const int page_vecs = static_cast<int>(p.page_bytes / 16), n32 = static_cast<int>(n);
+  const int per_page = (page_vecs + kStepVecs - 1) / kStepVecs;  // steps of a page
+  const int per_step = per_page > 1 ? 1 : kStepVecs / page_vecs;  // pages of a step
+  const int64_t pages = n * p.n_pools, all = (pages + per_step - 1) / per_step * per_page;
+  uint4 v[kCopyVecs];
   for (int64_t u = blockIdx.x; u < all; u += gridDim.x) {
-    const int64_t pg = u / steps;
-    const int step = static_cast<int>(u - pg * steps);
-    const int64_t i = pg % n, pool = pg / n;
-    const int from = __ldcg(src + i), to = __ldcg(dst + i);
-    if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages) {
-      if (threadIdx.x == 0) raise_status(status, kStatusBadId);
-      continue;
-    }
-    const uint8_t* a = p.base + pool * p.pool_stride + from * p.page_bytes;
-    uint8_t* b = p.base + pool * p.pool_stride + to * p.page_bytes;
-    uint4 v[kCopyVecs];
+    const int64_t first = u / per_page * per_step, pool0 = first / n;
+    const int i0 = static_cast<int>(first - pool0 * n);
+    if (per_step == 1) {
+      const int from = __ldg(src + i0), dest = __ldg(dst + i0);
+      if (from < 0 || from >= p.n_pages || dest < 0 || dest >= p.n_pages) {
+        if (threadIdx.x == 0) raise_status(status, kStatusBadId);
+        continue;
+      }
+      const int skip = static_cast<int>(u % per_page) * kStepVecs + threadIdx.x;
+      uint8_t* const base = p.base + pool0 * p.pool_stride + static_cast<int64_t>(skip) * 16;
+      const uint4* a = reinterpret_cast<const uint4*>(base + from * p.page_bytes);
+      uint4* b = reinterpret_cast<uint4*>(base + dest * p.page_bytes);
 #pragma unroll
-    for (int k = 0; k < kCopyVecs; ++k) {
-      const int64_t off = static_cast<int64_t>(step) * kCopyBytes + (k * kCopyThreads + threadIdx.x) * 16;
-      if (off < p.page_bytes) v[k] = __ldcs(reinterpret_cast<const uint4*>(a + off));
-    }
+      for (int k = 0; k < kCopyVecs; ++k)
+        if (skip + k * kCopyThreads < page_vecs) v[k] = __ldcs(a + k * kCopyThreads);
 #pragma unroll
-    for (int k = 0; k < kCopyVecs; ++k) {
-      const int64_t off = static_cast<int64_t>(step) * kCopyBytes + (k * kCopyThreads + threadIdx.x) * 16;
-      if (off < p.page_bytes) __stcs(reinterpret_cast<uint4*>(b + off), v[k]);
+      for (int k = 0; k < kCopyVecs; ++k)
+        if (skip + k * kCopyThreads < page_vecs) __stcs(b + k * kCopyThreads, v[k]);
+    } else {
+      uint4* to[kCopyVecs];
+#pragma unroll
+      for (int k = 0; k < kCopyVecs; ++k) {
+        const int at = k * kCopyThreads + static_cast<int>(threadIdx.x), sub = at / page_vecs;
+        to[k] = nullptr;
+        if (sub >= per_step || first + sub >= pages) continue;
+        const int more = (i0 + sub) / n32, i = i0 + sub - more * n32;
+        const int from = __ldg(src + i), dest = __ldg(dst + i);
+        if (from < 0 || from >= p.n_pages || dest < 0 || dest >= p.n_pages) {
+          raise_status(status, kStatusBadId);
+          continue;
+        }
+        uint8_t* const base = p.base + (pool0 + more) * p.pool_stride + (at - sub * page_vecs) * 16;
+        v[k] = __ldcs(reinterpret_cast<const uint4*>(base + from * p.page_bytes));
+        to[k] = reinterpret_cast<uint4*>(base + dest * p.page_bytes);
+      }
+#pragma unroll
+      for (int k = 0; k < kCopyVecs; ++k)
+        if (to[k]) __stcs(to[k], v[k]);
     }
   }
 }
@@ -505,7 +529,7 @@ bool launch_pdl(void (*kernel)(Params...), int grid, int threads, cudaStream_t s
   return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
-int copy_grid() { return 8 * device_info().num_sms; }
+int copy_grid() { return 2 * device_info().num_sms; }
 
 int launch_list_copy(const PagePool& p, const PagesWs& w, const int32_t* rank, unsigned* status, cudaStream_t s) {
   return launch_pdl(pages_copy_kernel, copy_grid(), kCopyThreads, s, p, static_cast<const int32_t*>(w.count), int64_t{0},
