@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagePo
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagePool p, const int32_t* count, int64_t n_fixed,
                                                                   const int32_t* src, const int32_t* dst,
                                                                   const int32_t* rank, unsigned* status) {
+  pdl_launch_dependents();  // one wave: the next call's plan may start and wait
   pdl_wait();
   const int64_t n = count ? __ldcg(count) : n_fixed;
   if (n == 0) return;

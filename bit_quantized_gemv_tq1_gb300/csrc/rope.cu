@@ -51,7 +51,7 @@ __device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
 // (of q, k and v) the blockIdx.y-th part of gridDim.y.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache c, const KvBatch b, const RopeArgs a,
-                                                                   int per, unsigned* status) {
+                                                                   int per, int one_wave, unsigned* status) {
   __shared__ float2 s_cs[kPer][kMaxRotPairs];
   __shared__ int s_seq[kPer], s_pos[kPer], s_page[kPer];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache
     h += stride;
     settle();
   };
+  if (one_wave) pdl_launch_dependents();
   pdl_wait();
   fetch();  // on their way while the tokens' places are looked up
   // The sequence of each token, its position and its page: a warp per token.
@@ -211,7 +212,7 @@ int launch(const KvCache& c, const KvBatch& b, const RopeArgs& a, unsigned* stat
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cuda_ok(cudaLaunchKernelEx(&cfg, rope_append_kernel<TI, TO>, c, b, a, per, status)) ? TQ1_OK : TQ1_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, rope_append_kernel<TI, TO>, c, b, a, per, gx * gy <= 2 * sms ? 1 : 0, status)) ? TQ1_OK : TQ1_ERR_CUDA;
 }
 
 template <typename TO>
