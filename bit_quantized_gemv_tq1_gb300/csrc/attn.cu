@@ -16,6 +16,11 @@
 // waits for another warp.  The products run on mma.sync (16 x 8 x 16): 64
 // instructions per 16 keys and warp, far from a limit here, where a
 // 128-row tensor-core tile would be at most 1/8 full.
+// 64 sequences of 223 000 keys in all, 40/8 heads of 128: 152 us, 6.1 TB/s;
+// one of 131 071, 32/4 heads: 50 us, 5.3 TB/s (the median CTA is done at
+// 38 us, the last at 44: the SMs' shares of the bandwidth are not equal, and
+// finer shares cost more in starts than they even out: 65 us with four per
+// SM); one of 777: 8 us, the latency of two launches.
 #include <algorithm>
 #include <atomic>
 
@@ -378,7 +383,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
 // chunks): a thread per piece of 4 columns.  Few rows in many parts (a decode
 // step over a long cache has one tile in 40): the CTA's warps share the parts
 // out, 32 pieces at a time, and their sums meet in shared memory.  Fixed
-// order: the same sums every time.
+// order: the same sums every time.  Bound by latency: the parts are in L2; one
+// sequence of 131 071 keys (40 parts a tile) adds 2 us to the call.
 constexpr int kJoinWarps = 8;
 
 struct RowSum {
@@ -445,6 +451,11 @@ namespace {
 // Which kernel a call takes, by the rows (tokens x query heads of a kv head)
 // of an average sequence: kWarps for up to one 16-row tile, else the 128-row
 // kernel, with two such tiles side by side where one does not hold them.
+// Measured, 32 sequences of 2000 keys, 32/8 heads of 128 (of 64), us:
+//   rows        4           16           20            128           136
+//   kWarps      50 (30)     53 (33)      101 (62)      326 (181)     366 (200)
+//   kTile       52 (37)     53 (37)      53 (38)       64 (41)       112 (75)
+//   kTilePair   56 (47)     57 (48)      57 (48)       68 (50)       70 (51)
 enum Route { kWarps, kTile, kTilePair };
 Route route(int64_t t, int64_t group, int64_t n_seqs) {
   const int64_t rows = (t * group + n_seqs - 1) / n_seqs;

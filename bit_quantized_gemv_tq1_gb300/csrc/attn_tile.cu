@@ -12,7 +12,16 @@
 // Bound: the tensor pipe.  Per 128 x 128 keys it takes 8 d cycles for both
 // products (4096 multiply-adds a cycle), the exponentials 512; so two streams
 // of (S, P, O), one warp group each, take turns: while one's weights are
-// formed the tensor pipe does the other's products.
+// formed the tensor pipe does the other's products.  What it comes to is the
+// latency of a stream's chain, which one block after the other goes through:
+// at d = 128 some 1400 cycles for a block's weights (450 to read the scores
+// and find the maximum, 800 for the exponentials, 110 to store them), 1024 in
+// the tensor pipe and 400 between the roles, against 2048 of tensor work for
+// both streams.  S and P of a second block per stream would break the chain;
+// the two O leave no tensor memory for them.
+// 4096 tokens on 12288 keys, 40/8 heads of 128: 555 us, 1.55 PFLOP/s at the
+// power limit's 1.95 GHz.  A ragged batch (1 to 1463 tokens, 24/8 heads of 64,
+// window 1024): 53 us, of which 8 pass before the first scores.
 //   PAIR:  a tile has two times 128 rows, a stream each, and both read the
 //          same keys (a chunk with more than 128 rows per kv head)
 //   else:  a tile has 128 rows; the streams take every other block and are
@@ -59,7 +68,7 @@ struct TileCfg {
   static constexpr uint32_t kHalf = kTBlock * 128;             // 64 elements of 128 rows
   static constexpr uint32_t kTile = (D / 64) * kHalf;          // 128 rows of q, keys or values
   static constexpr int kQTiles = PAIR ? 2 : 1;
-  static constexpr uint32_t kStatic = PAIR ? 1536 : 3584;      // barriers, and the streams' join
+  static constexpr uint32_t kStatic = PAIR ? 1536 : 3584;      // at most: barriers, segments, the streams' join
   static constexpr int kRing = static_cast<int>((232448 - kStatic - 1024) / kTile) - kQTiles;
   static constexpr uint32_t kSmem = (kQTiles + kRing) * kTile + 1024;
   // A stream's next block.  Blocks of keys are copied so many blocks ahead of
@@ -67,7 +76,7 @@ struct TileCfg {
   //   PAIR: K0 V0 K1 V1 K2 ...      else: K0 K1 V0 K2 V1 K3 V2 ...
   static constexpr int kStep = PAIR ? 1 : 2;
   static __device__ __forceinline__ uint32_t value_slot(int i, int n) { return PAIR ? 2 * i + 1 : i + min(i + 2, n); }
-  static constexpr uint32_t kS = 0, kO = 256;  // tensor-memory columns: S of stream s at 128 s, O at kO + s D
+  static constexpr uint32_t kO = 256;  // tensor-memory columns: S of stream s at 128 s, O at kO + s D
 };
 
 struct TileKernelArgs {
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
     const int s = (warp >> 2) - 1, row = tid & (kTRows - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t st_at = tmem + lanes + C::kS + 128 * s, o_at = tmem + lanes + C::kO + s * D;
+    const uint32_t st_at = tmem + lanes + 128 * s, o_at = tmem + lanes + C::kO + s * D;
     const float sc = k.a.scale * kLog2e;
     uint32_t done = 0;   // blocks this stream has done, over all segments
     uint32_t oph = 0;    // phase of o_full
@@ -542,13 +551,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
-          umma_ss(tmem + C::kS + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+          umma_ss(tmem + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
         }
         umma_commit(&s_full[s]);
       };
       // Keys in steps of 16, [from, steps) of them.
       auto product_o = [&](int s, uint32_t slot, int from, int steps, uint32_t keep) {
-        const uint32_t s_col = tmem + C::kS + 128 * s, o_col = tmem + C::kO + s * D;
+        const uint32_t s_col = tmem + 128 * s, o_col = tmem + C::kO + s * D;
         const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
         if (from == 0 && steps == kTBlock / 16) {
 #pragma unroll
