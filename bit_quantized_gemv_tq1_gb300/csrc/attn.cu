@@ -16,7 +16,7 @@
 // waits for another warp.  The products run on mma.sync (16 x 8 x 16): 64
 // instructions per 16 keys and warp, far from a limit here, where a
 // 128-row tensor-core tile would be at most 1/8 full.
-// 64 sequences of 223 000 keys in all, 40/8 heads of 128: 152 us, 6.1 TB/s;
+// 64 sequences of 223 000 keys in all, 40/8 heads of 128: 146 us, 6.3 TB/s;
 // one of 131 071, 32/4 heads: 50 us, 5.3 TB/s (the median CTA is done at
 // 38 us, the last at 44: the SMs' shares of the bandwidth are not equal, and
 // finer shares cost more in starts than they even out: 65 us with four per
@@ -218,13 +218,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
     // steps requested behind cur's last: the copies go on while the warps are
     // joined (without this a CTA stood still for some 3 us per tile, of which
     // a batch of 64 sequences has 3.4 a CTA).
-    const bool more = left > cur.todo;
+    const bool more = left > cur.todo + kTileCost;
     int ids_n = -1;
     if (more) {
       nxt = cur;
       next_tile(plan, b, nxt.head, nxt.seq, nxt.tile, nxt.sq);
       nxt.blk = 0;
-      open(nxt, left - cur.todo);
+      open(nxt, left - cur.todo - kTileCost);
       ids_n = pages_of(nxt, 0);
     }
     const bool flows = more && cur.todo >= kAhead && nxt.todo >= kAhead;
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
     if (!whole && cur.blk == 0 && tid == 0)
       parts[slot] = Part{cur.head, cur.sq.q0, row0, rows, share_of(st.work, st.used, unit + cur.nb - 1), {}};
     if (!more) break;
-    left -= cur.todo;
-    unit += cur.todo;
+    left -= cur.todo + kTileCost;
+    unit += cur.todo + kTileCost;
     base += cur.todo;
     cur = nxt;
     ids = ids_n;

@@ -62,14 +62,28 @@ __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
 // are its rows, row = token * group + head, cut into tiles of `rows` rows.
 // A tile reads the cache in blocks of `block` keys, from the first key any
 // of its rows sees to the last.  The call's work is the list of (kv head,
-// sequence, tile, block), in that order; CTA c of C does the units
+// sequence, tile, block), in that order, where a tile's blocks come after
+// kTileCost units for its beginning and end; CTA c of C does the units
 // [W c / C, W (c+1) / C) of the W in the list.  So every CTA has the same
 // work to one unit whatever the sequences' lengths are, and only the tiles at
-// a CTA's two ends are shared: their parts are joined afterwards.
+// a CTA's two ends are shared: their parts are joined afterwards.  (A share
+// that ends within a tile's cost does nothing of the tile, and one that begins
+// there begins with its first block.)
 struct TilePlan {
   int rows, group, causal, window;
   int shift;  // log2 of a block's keys
 };
+
+// What a tile costs beside its blocks, in blocks: its queries, the first
+// block's latency, the last product, its output (2 us of the tensor-core
+// kernel).  Without it a CTA with six tiles was done 6 us after one with three
+// (ragged mix of 1 to 1463 tokens, us with 0 / 1 / 2 / 3 / 4 / 6: 53.2 / 48.9 /
+// 48.5 / 47.5 / 47.3 / 48.2; decode step of 64 sequences: 153 / 148 / 146 /
+// 145 / 146 / 151; 12 sequences of up to 1500 tokens and 5000 keys, 24/8 heads
+// of 128: 167 / 156 / 150 / 146 / 148 / 151).  Calls that give a CTA a few
+// blocks are divided less evenly by it: three sequences of 30 to 90 tokens
+// 20.0 us with 0 to 2, 21.2 with 3.
+constexpr int kTileCost = 3;
 
 // Blocks of one tile: the first one and how many.  A tile whose rows see
 // nothing has one block (it is masked whole; its rows come out as zeros).
@@ -121,7 +135,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
 // Where CTA `cta` of `ctas` begins and how much it does.
 struct Start {
   int head, seq, tile, block;  // first unit
-  int64_t first, units;        // its place in the list, units of this CTA (0: none)
+  int64_t first, units;        // its place in the list, units of this CTA from there on (0: none)
   int64_t work;                // units of the call
   int used;                    // CTAs that have some
   Seq sq;                      // of `seq`
@@ -159,7 +173,10 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       const Seq q = load_seq(b, s);
       const int tiles = seq_tiles(p, q);
       int f;
-      if (tiles == 1) tile_blocks(p, q, 0, f, nb);
+      if (tiles == 1) {
+        tile_blocks(p, q, 0, f, nb);
+        nb += kTileCost;
+      }
       if (tiles > 1) nb = -1;
       s_nb[s] = nb;
     }
@@ -172,7 +189,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       for (int i = lane; i < tiles; i += 32) {
         int f, c;
         tile_blocks(p, q, i, f, c);
-        sum += c;
+        sum += c + kTileCost;
       }
       sum = warp_scan(sum);
       if (lane == 31) s_nb[t] = sum;
@@ -185,7 +202,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) mine += s_nb[s];
   const int64_t end = warp_scan(mine);
-  const int64_t all = __shfl_sync(0xffffffffu, end, 31);  // blocks of one kv head
+  const int64_t all = __shfl_sync(0xffffffffu, end, 31);  // units of one kv head
   Start r;
   const int64_t work = all * n_kv;
   const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
@@ -213,7 +230,10 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   r.block = static_cast<int>(rem);
   for (int base = 0; tiles > 1 && base < tiles; base += 32) {
     int f, c = 0;
-    if (base + lane < tiles) tile_blocks(p, q, base + lane, f, c);
+    if (base + lane < tiles) {
+      tile_blocks(p, q, base + lane, f, c);
+      c += kTileCost;
+    }
     const int upto = warp_scan(c), sum = __shfl_sync(0xffffffffu, upto, 31);
     if (rem < sum) {
       const int hit = __ffs(__ballot_sync(0xffffffffu, rem < upto)) - 1;
@@ -223,6 +243,11 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
     }
     rem -= sum;
   }
+  // From the tile's units to its blocks.
+  const int rest = max(kTileCost - r.block, 0);
+  r.block = max(r.block - kTileCost, 0);
+  r.first += rest;
+  r.units = max(r.units - rest, int64_t{0});
   return r;
 }
 

@@ -176,6 +176,14 @@ def test_many_sequences():
     check(Batch(new, [max(v, (i * 37) % 90) for i, v in enumerate(new)], 16, 1, 64, F16), 2)
 
 
+@pytest.mark.parametrize("n", [1, 2, 37, 38, 39, 75, 76, 77, 151, 152, 153])
+@pytest.mark.parametrize("new,d", [(1, 64), (1, 128), (6, 64), (40, 128)])
+def test_about_as_many_blocks_as_ctas(n, new, d):
+    # Shares of one unit and a little more: some begin or end between two tiles
+    # and do nothing of either.
+    check(Batch([new] * n, [new + (i * 53) % 300 for i in range(n)], 16, 1, d, F16, seed=n, junk=float("nan")), 4)
+
+
 def test_offsets_past_32_bits():
     # A pool of more than 2^32 bytes of keys; the sequence's pages are its last.
     L = lib()
