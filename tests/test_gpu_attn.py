@@ -176,6 +176,24 @@ def test_many_sequences():
     check(Batch(new, [max(v, (i * 37) % 90) for i, v in enumerate(new)], 16, 1, 64, F16), 2)
 
 
+@pytest.mark.parametrize("off,pad", [(0, 8), (8, 16), (16, 32), (8, 8)])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("new", [2, 30, 200])
+def test_output_rows_of_a_wider_matrix(new, f32, off, pad):
+    # Rows that begin on 16-byte boundaries, or on 32-byte ones too.
+    b = Batch([new, new], [new + 100, new + 333], 16, 2, 64, F16)
+    b.to_gpu(lib())
+    q, gq = queries(b, 6)
+    room = torch.full((b.t, off + 6 * 64 + pad), 7.0, dtype=torch.float32 if f32 else F16, device="cuda")
+    out = room[:, off:off + 6 * 64].unflatten(1, (6, 64))
+    ws = torch.empty(lib().tq1_paged_attn_workspace_size(b.cache, b.t, 6, 2), dtype=torch.uint8, device="cuda")
+    lib().tq1_paged_attn(b.cache, b.batch, gq, out, 0.125, ws=ws)
+    assert lib().tq1_sync_status() == 0
+    ref, tol = attention(b, q, 0.125, True, 0)
+    assert ((out.cpu().double() - ref).abs() <= rounded(tol, ref, out.dtype)).all()
+    assert (room[:, :off] == 7).all() and (room[:, off + 6 * 64:] == 7).all()
+
+
 @pytest.mark.parametrize("n", [1, 2, 37, 38, 39, 75, 76, 77, 151, 152, 153])
 @pytest.mark.parametrize("new,d", [(1, 64), (1, 128), (6, 64), (40, 128)])
 def test_about_as_many_blocks_as_ctas(n, new, d):
