@@ -218,13 +218,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
     // steps requested behind cur's last: the copies go on while the warps are
     // joined (without this a CTA stood still for some 3 us per tile, of which
     // a batch of 64 sequences has 3.4 a CTA).
-    const bool more = left > cur.todo + kTileCost;
+    const bool more = left > cur.todo + st.cost;
     int ids_n = -1;
     if (more) {
       nxt = cur;
       next_tile(plan, b, nxt.head, nxt.seq, nxt.tile, nxt.sq);
       nxt.blk = 0;
-      open(nxt, left - cur.todo - kTileCost);
+      open(nxt, left - cur.todo - st.cost);
       ids_n = pages_of(nxt, 0);
     }
     const bool flows = more && cur.todo >= kAhead && nxt.todo >= kAhead;
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
     if (!whole && cur.blk == 0 && tid == 0)
       parts[slot] = Part{cur.head, cur.sq.q0, row0, rows, share_of(st.work, st.used, unit + cur.nb - 1), {}};
     if (!more) break;
-    left -= cur.todo + kTileCost;
-    unit += cur.todo + kTileCost;
+    left -= cur.todo + st.cost;
+    unit += cur.todo + st.cost;
     base += cur.todo;
     cur = nxt;
     ids = ids_n;

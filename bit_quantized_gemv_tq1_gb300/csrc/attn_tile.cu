@@ -745,8 +745,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         __syncwarp();
         if (more) {
-          left -= g.todo + kTileCost;
-          unit += g.todo + kTileCost;
+          left -= g.todo + st.cost;
+          unit += g.todo + st.cost;
           if (left > 0) {
             next_tile(k.plan, k.b, head, seq, tile, sq);
             blk = 0;

@@ -63,7 +63,7 @@ __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
 // A tile reads the cache in blocks of `block` keys, from the first key any
 // of its rows sees to the last.  The call's work is the list of (kv head,
 // sequence, tile, block), in that order, where a tile's blocks come after
-// kTileCost units for its beginning and end; CTA c of C does the units
+// `cost` units for its beginning and end; CTA c of C does the units
 // [W c / C, W (c+1) / C) of the W in the list.  So every CTA has the same
 // work to one unit whatever the sequences' lengths are, and only the tiles at
 // a CTA's two ends are shared: their parts are joined afterwards.  (A share
@@ -80,9 +80,10 @@ struct TilePlan {
 // (ragged mix of 1 to 1463 tokens, us with 0 / 1 / 2 / 3 / 4 / 6: 53.2 / 48.9 /
 // 48.5 / 47.5 / 47.3 / 48.2; decode step of 64 sequences: 153 / 148 / 146 /
 // 145 / 146 / 151; 12 sequences of up to 1500 tokens and 5000 keys, 24/8 heads
-// of 128: 167 / 156 / 150 / 146 / 148 / 151).  Calls that give a CTA a few
-// blocks are divided less evenly by it: three sequences of 30 to 90 tokens
-// 20.0 us with 0 to 2, 21.2 with 3.
+// of 128: 167 / 156 / 150 / 146 / 148 / 151).  Shares of so few blocks that
+// a tile's cost is most of them want one less (decode step of 8 sequences of
+// 200 to 900 keys, us with 0 / 1 / 2 / 3: 11.8 / 11.5 / 10.6 / 10.9; three
+// chunks of 30 to 90 tokens: 20.0 / 19.9 / 19.9 / 21.2).
 constexpr int kTileCost = 3;
 
 // Blocks of one tile: the first one and how many.  A tile whose rows see
@@ -138,6 +139,7 @@ struct Start {
   int64_t first, units;        // its place in the list, units of this CTA from there on (0: none)
   int64_t work;                // units of the call
   int used;                    // CTAs that have some
+  int cost;                    // units of a tile beside its blocks
   Seq sq;                      // of `seq`
 };
 
@@ -156,15 +158,16 @@ __device__ __forceinline__ int share_of(int64_t work, int used, int64_t u) {
   return static_cast<int>(u < longer ? u / (q + 1) : r + (u - longer) / q);
 }
 
-// Called by all NT threads; every warp has the result.  `s_nb`: at least
-// n_seqs words of shared memory, still read by other warps when the call
+// Called by all NT threads; every warp has the result.  `s_nb`: at least 12
+// n_seqs bytes of shared memory, still read by other warps when the call
 // returns.  One barrier: the search stands before anything else of the call,
 // and of a small call it was the larger part (a form with a block-wide sum per
 // step took 5 us of the 70 us of a ragged batch of prompt chunks).
 template <int NT>
 __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int64_t* s_nb) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Blocks of each sequence: by its thread where it has one tile, else (left
+  int* const s_nt = reinterpret_cast<int*>(s_nb + b.n_seqs);
+  // Blocks and tiles of each sequence: by its thread where it has one tile, else (left
   // as -1) by a warp, a lane per tile.
   for (int s0 = 32 * warp; s0 < b.n_seqs; s0 += NT) {
     const int s = s0 + lane;
@@ -173,12 +176,10 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       const Seq q = load_seq(b, s);
       const int tiles = seq_tiles(p, q);
       int f;
-      if (tiles == 1) {
-        tile_blocks(p, q, 0, f, nb);
-        nb += kTileCost;
-      }
+      if (tiles == 1) tile_blocks(p, q, 0, f, nb);
       if (tiles > 1) nb = -1;
       s_nb[s] = nb;
+      s_nt[s] = tiles;
     }
     __syncwarp();
     for (uint32_t more = __ballot_sync(0xffffffffu, nb < 0); more; more &= more - 1) {
@@ -189,7 +190,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       for (int i = lane; i < tiles; i += 32) {
         int f, c;
         tile_blocks(p, q, i, f, c);
-        sum += c + kTileCost;
+        sum += c;
       }
       sum = warp_scan(sum);
       if (lane == 31) s_nb[t] = sum;
@@ -200,10 +201,19 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   // whose run holds the first unit.
   const int run = (b.n_seqs + 31) >> 5, s0 = lane * run, s1 = min(s0 + run, b.n_seqs);
   int64_t mine = 0;
-  for (int s = s0; s < s1; ++s) mine += s_nb[s];
-  const int64_t end = warp_scan(mine);
-  const int64_t all = __shfl_sync(0xffffffffu, end, 31);  // units of one kv head
+  int mine_t = 0;
+  for (int s = s0; s < s1; ++s) {
+    mine += s_nb[s];
+    mine_t += s_nt[s];
+  }
+  int64_t end = warp_scan(mine);
+  const int end_t = warp_scan(mine_t);
+  int64_t all = __shfl_sync(0xffffffffu, end, 31);  // blocks of one kv head
   Start r;
+  r.cost = all * n_kv < static_cast<int64_t>(kTileCost) * ctas ? kTileCost - 1 : kTileCost;
+  mine += static_cast<int64_t>(r.cost) * mine_t;
+  end += static_cast<int64_t>(r.cost) * end_t;
+  all += static_cast<int64_t>(r.cost) * __shfl_sync(0xffffffffu, end_t, 31);  // units of one kv head
   const int64_t work = all * n_kv;
   const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
   r.work = work;
@@ -221,7 +231,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   int seq = s0;
   int64_t into = rem - (end - mine);
   if (lane == owner)
-    while (into >= s_nb[seq]) into -= s_nb[seq++];
+    for (int64_t u; into >= (u = s_nb[seq] + static_cast<int64_t>(r.cost) * s_nt[seq]); ++seq) into -= u;
   r.seq = __shfl_sync(0xffffffffu, seq, owner);
   rem = __shfl_sync(0xffffffffu, into, owner);
   const Seq q = load_seq(b, r.seq);
@@ -232,7 +242,7 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
     int f, c = 0;
     if (base + lane < tiles) {
       tile_blocks(p, q, base + lane, f, c);
-      c += kTileCost;
+      c += r.cost;
     }
     const int upto = warp_scan(c), sum = __shfl_sync(0xffffffffu, upto, 31);
     if (rem < sum) {
@@ -244,8 +254,8 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
     rem -= sum;
   }
   // From the tile's units to its blocks.
-  const int rest = max(kTileCost - r.block, 0);
-  r.block = max(r.block - kTileCost, 0);
+  const int rest = max(r.cost - r.block, 0);
+  r.block = max(r.block - r.cost, 0);
   r.first += rest;
   r.units = max(r.units - rest, int64_t{0});
   return r;
