@@ -163,10 +163,8 @@ def _current_stream():
     except AttributeError:
         return lambda: torch.cuda.current_stream().cuda_stream
 
-    def current() -> int:
-        torch.cuda._lazy_init()
-        return raw(device())
-    return current
+    torch.cuda.init()
+    return lambda: raw(device())
 
 
 _current = None
@@ -444,9 +442,10 @@ def tq1_rope_append(cache, batch, q, k, v, q_out, inv_freq, rot_dim: int, interl
     pq, ldq, t, n_q = _rows(q, None, d, "q")
     pk, ldk, tk, _ = _rows(k, n_kv, d, "k")
     pv, ldv, tv, _ = _rows(v, n_kv, d, "v")
-    if tk != t or tv != t or not (q.dtype is k.dtype is v.dtype):
+    dtype = q.dtype
+    if tk != t or tv != t or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k and v: one type and one number of tokens")
-    if q_out.shape != q.shape or _dtype(q_out) != cache.dtype:
+    if q_out.shape != (t, n_q, d) or _dtype(q_out) != cache.dtype:
         raise ValueError("q_out: q's shape and the cache's type")
     if inv_freq is not None and (inv_freq.numel() != rot_dim // 2 or _dtype(inv_freq) != TQ1_F32):
         raise ValueError(f"inv_freq: expected {rot_dim // 2} fp32 values")
@@ -499,13 +498,15 @@ def tq1_pages_copy(pool, src, dst, stream=None) -> None:
 
 def tq1_pages_resize(pool, seqs, new_len, ws, stream=None) -> None:
     """Set the length of sequences seqs[i] to new_len[i]: pages are freed, given, and copied where shared."""
-    _check(library().tq1_pages_resize(pool, _ints(seqs), _ints(new_len, seqs.numel()), seqs.numel(), _addr(ws),
+    n = seqs.numel()
+    _check(library().tq1_pages_resize(pool, _ints(seqs), _ints(new_len, n), n, _addr(ws),
                                       ws.numel() * ws.element_size(), _stream(stream)), "tq1_pages_resize")
 
 
 def tq1_pages_fork(pool, parents, children, ws, stream=None) -> None:
     """The empty sequences children[i] become copies of parents[i], sharing their full pages."""
-    _check(library().tq1_pages_fork(pool, _ints(parents), _ints(children, parents.numel()), parents.numel(), _addr(ws),
+    n = parents.numel()
+    _check(library().tq1_pages_fork(pool, _ints(parents), _ints(children, n), n, _addr(ws),
                                     ws.numel() * ws.element_size(), _stream(stream)), "tq1_pages_fork")
 
 
