@@ -16,8 +16,8 @@
 // waits for another warp.  The products run on mma.sync (16 x 8 x 16): 64
 // instructions per 16 keys and warp, far from a limit here, where a
 // 128-row tensor-core tile would be at most 1/8 full.
-// 64 sequences of 223 000 keys in all, 40/8 heads of 128: 146 us, 6.3 TB/s;
-// one of 131 071, 32/4 heads: 50 us, 5.3 TB/s (the median CTA is done at
+// 64 sequences of 223 000 keys in all, 40/8 heads of 128: 144 us, 6.4 TB/s;
+// one of 131 071, 32/4 heads: 49 us, 5.5 TB/s (the median CTA is done at
 // 38 us, the last at 44: the SMs' shares of the bandwidth are not equal, and
 // finer shares cost more in starts than they even out: 65 us with four per
 // SM); one of 777: 8 us, the latency of two launches.
@@ -404,7 +404,7 @@ struct RowSum {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    attn_join_kernel(const AttnArgs a, int slot_rows, int group, const Part* parts, const float* slots) {
+    attn_join_kernel(const AttnArgs a, int slot_rows, const Divisor group, const Part* parts, const float* slots) {
   __shared__ float s_m[kJoinWarps][32], s_l[kJoinWarps][32];
   __shared__ float4 s_v[kJoinWarps][32];
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -492,7 +492,7 @@ int launch_warp(const KvCache& c, const KvBatch& b, const AttnArgs& a, int ctas,
       return TQ1_ERR_CUDA;
     configured[di.device].store(true, std::memory_order_release);
   }
-  const TilePlan plan = {kARows, a.n_q / c.n_kv, a.causal, a.window, kAShift};
+  const TilePlan plan = {Divisor(kARows), Divisor(a.n_q / c.n_kv), a.causal, a.window, kAShift};
   return launch_pdl(attn_warp_kernel<T, D>, dim3(ctas), kAThreads, C::kSmem, s, c, b, a, plan, parts, slots, status)
              ? TQ1_OK
              : TQ1_ERR_CUDA;
@@ -512,8 +512,8 @@ int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a,
   }
   if (rc != TQ1_OK) return rc;
   const int rows = route_rows(r, group);
-  const int share = std::min(8, (rows * (D / 4) + 31) / 32);  // 8 CTAs an SM: all resident at once
-  return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 32 * kJoinWarps, 0, s, a, rows, group,
+  const int share = std::min(8, (rows * (D / 4) + 31) / 32);  // CTAs that share out a tile's rows
+  return launch_pdl(attn_join_kernel<T, D>, dim3(ctas, share), 32 * kJoinWarps, 0, s, a, rows, Divisor(group),
                     static_cast<const Part*>(parts), static_cast<const float*>(slots))
              ? TQ1_OK
              : TQ1_ERR_CUDA;

@@ -19,9 +19,9 @@
 // the tensor pipe and 400 between the roles, against 2048 of tensor work for
 // both streams.  S and P of a second block per stream would break the chain;
 // the two O leave no tensor memory for them.
-// 4096 tokens on 12288 keys, 40/8 heads of 128: 555 us, 1.55 PFLOP/s at the
-// power limit's 1.95 GHz.  A ragged batch (1 to 1463 tokens, 24/8 heads of 64,
-// window 1024): 46.6 us, of which 5 pass before the first scores.
+// 4096 tokens on 12288 keys, 40/8 heads of 128: 550 us, 1.56 PFLOP/s, and
+// 586 call after call, at the power limit's lower clock.  A ragged batch (1 to 1463 tokens, 24/8 heads of 64,
+// window 1024): 45.3 us, of which 5 pass before the first scores.
 //   PAIR:  a tile has two times 128 rows, a stream each, and both read the
 //          same keys (a chunk with more than 128 rows per kv head)
 //   else:  a tile has 128 rows; the streams take every other block and are
@@ -309,7 +309,222 @@ __global__ void __launch_bounds__(kTThreads, 1)
     return true;
   };
 
-  if (warp >= 4) {
+  // The weights' branch is the last in the text: where the roles' loops come
+  // to lie is worth 2% (chunk, call after call: 600 us with it first, 586 so).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kMmaWarp) {
+      // ----------------------------------------------------------- MMA --
+      // In a step (a block's second product and the first product kStep
+      // blocks on) the streams take turns; issued from a warp each, their
+      // instructions would interleave and both streams' products finish late
+      // (4096 tokens on 12288 keys, 40/8 heads of 128: 670 us for 560).
+      //
+      // The whole warp walks the loop without a branch on what a lane has
+      // seen (wait_soft), and one lane issues: addresses and descriptors are
+      // then the same in all lanes to the compiler too, which keeps them in
+      // the uniform registers that the instructions take.
+      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
+      constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
+      const bool lead = elect_one();
+      const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
+      const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
+      uint32_t pph = 0, qph = 0;   // phases of p_full (a bit per stream) and q_full
+      uint32_t ri = 0, rph = 0;    // ring slot to be consumed next, its phase
+      auto step = [&]() {
+        if (++ri == C::kRing) {
+          ri = 0;
+          rph ^= 1u;
+        }
+      };
+      auto product_s = [&](int s, uint32_t slot) {
+        const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
+          umma_ss(tmem + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[s]);
+      };
+      // Keys in steps of 16, [from, steps) of them.
+      auto product_o = [&](int s, uint32_t slot, int from, int steps, uint32_t keep) {
+        const uint32_t s_col = tmem + 128 * s, o_col = tmem + C::kO + s * D;
+        const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
+        if (from == 0 && steps == kTBlock / 16) {
+#pragma unroll
+          for (int ks = 0; ks < kTBlock / 16; ++ks)
+            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
+        } else {
+          for (int ks = from; ks < steps; ++ks)
+            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > from ? 1u : keep);
+        }
+      };
+      for (uint32_t at = 0;; ++at) {
+        wait_soft(&seg_full[at % kSegs], (at / kSegs) & 1u, &s_abort);
+        const int n = uniform(*abort_flag ? 0 : s_seg[at % kSegs].todo), none = uniform(s_seg[at % kSegs].empty);
+        const int first_key = uniform(s_seg[at % kSegs].first_key), hi = uniform(s_seg[at % kSegs].hi);
+        const int lo = uniform(s_seg[at % kSegs].lo);
+        if (lead) mbar_arrive(&seg_empty[at % kSegs]);
+        if (n == 0) break;
+        if (none) continue;
+        wait_soft(&q_full, qph, &s_abort);
+        qph ^= 1u;
+#pragma unroll
+        for (int i = 0; i < C::kStep; ++i) {
+          if (i >= n) break;
+          wait_soft(&full[ri], rph, &s_abort);
+          tc_fence_after();
+          if (lead) {
+            product_s(PAIR ? 0 : i, ri);
+            if (PAIR) product_s(1, ri);
+            umma_commit(&empty[ri]);
+          }
+          step();
+        }
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + C::kStep < n;
+          // The last first product is on its way.
+          if (lead && (i + C::kStep == n || (i == 0 && n < C::kStep))) umma_commit(&q_empty);
+          const int key0 = first_key + i * kTBlock;
+          const int steps = (min(kTBlock, hi - key0) + 15) >> 4, from = max(0, lo - key0) >> 4;
+          const uint32_t slot = ri, sph = rph;
+          step();
+          const uint32_t nslot = ri, nph = rph;
+          if (more) step();
+          wait_soft(&full[slot], sph, &s_abort);
+          if (more) wait_soft(&full[nslot], nph, &s_abort);
+#pragma unroll
+          for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
+            const int s = PAIR ? u : (i & 1);
+            wait_soft(&p_full[s], (pph >> s) & 1u, &s_abort);
+            pph ^= 1u << s;
+            tc_fence_after();
+            if (lead) {
+              product_o(s, slot, from, steps, i >= C::kStep ? 1u : 0u);
+              if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
+              if (more) {
+                product_s(s, nslot);
+                if (u == (PAIR ? 1 : 0)) umma_commit(&empty[nslot]);
+              } else {
+                umma_commit(&o_full[s]);
+              }
+            }
+          }
+        }
+      }
+      // After an abort, let the products already issued finish (bounded).
+      __syncwarp();
+      if (*abort_flag) {
+        if (lead) umma_commit(&drained);
+        (void)mbar_wait(&drained, 0);
+      }
+    } else if (warp == kLoadWarp) {
+      // --------------------------------------------------------- copies --
+      uint32_t at = 0, segs = 0;  // ring slots filled, segments read
+      bool ok = true;
+      const int boxes = kTBlock / k.box_keys;  // of a block
+      const int half = lane & (D / 64 - 1), box = lane / (D / 64);
+      // The page of this lane's box of the block from key0 on: -1 (read as
+      // zeros) where the table names none, -2 past the sequence's end.
+      auto page_of = [&](int key0) {
+        const int key = key0 + box * k.box_keys;
+        if (box >= boxes || key >= g.len) return -2;
+        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
+        if (id >= 0 && id < k.c.n_pages) return id;
+        raise_status(k.status, kStatusBadId);
+        return -1;
+      };
+      auto copy = [&](const CUtensorMap* map, int key0, int page) {
+        const uint32_t slot = at % C::kRing;
+        if (!(ok = wait_all(&empty[slot], ((at / C::kRing) & 1u) ^ 1u, abort_flag))) return false;
+        const uint32_t live = __ballot_sync(0xffffffffu, page != -2);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * k.box_keys * 128);
+        __syncwarp();
+        if (page != -2)
+          tma_load_4d(ring_at + slot * C::kTile + half * C::kHalf + box * k.box_keys * 128, map, 64 * half,
+                      (key0 + box * k.box_keys) & (k.c.page_size - 1), g.head, page, &full[slot]);
+        ++at;
+        return true;
+      };
+      while (ok && next_segment() && g.todo > 0) {
+        if (g.empty) continue;
+        int page[C::kStep];
+#pragma unroll
+        for (int i = 0; i < C::kStep; ++i) page[i] = i < g.todo ? page_of(g.first_key + i * kTBlock) : -2;
+        if (!(ok = wait_all(&q_empty, (segs & 1u) ^ 1u, abort_flag))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, C::kQTiles * (D / 64) * k.stream_rows * 128);
+        __syncwarp();
+        if (lane < C::kQTiles * (D / 64)) {
+          const int qs = lane / (D / 64), qhalf = lane & (D / 64 - 1);
+          tma_load_3d(q_at + qs * C::kTile + qhalf * C::kHalf, &tmq, 64 * qhalf, g.head * k.plan.group,
+                      g.q0 + g.tok0 + qs * k.stream_tokens, &q_full);
+        }
+        ++segs;
+        for (int i = 0; i < C::kStep && i < g.todo && ok; ++i) copy(&tmk, g.first_key + i * kTBlock, page[i]);
+        for (int i = 0; i < g.todo && ok; ++i) {
+          const int next = i + C::kStep, key = g.first_key + i * kTBlock;
+          const int np = next < g.todo ? page_of(g.first_key + next * kTBlock) : -2;
+          if (!copy(&tmv, key, page[0])) break;
+          if (next < g.todo && !copy(&tmk, g.first_key + next * kTBlock, np)) break;
+#pragma unroll
+          for (int j = 0; j + 1 < C::kStep; ++j) page[j] = page[j + 1];
+          page[C::kStep - 1] = np;
+        }
+      }
+      // Copies still in flight must land before the CTA leaves.
+      if (lane == 0 && *abort_flag) {
+        for (uint32_t i = at > C::kRing ? at - C::kRing : 0; i < at; ++i)
+          (void)mbar_wait(&full[i % C::kRing], (i / C::kRing) & 1u);
+        if (segs) (void)mbar_wait(&q_full, (segs - 1) & 1u);
+      }
+    } else if (warp == kPlanWarp) {
+      // ----------------------------------------------------------- plan --
+      int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
+      int64_t left = st.units, unit = st.first;
+      Seq sq = st.sq;
+      for (bool more = true; more; ++seg_at) {
+        g = Segment{};
+        more = left > 0;
+        if (more) {
+          int fb, nb;
+          tile_blocks(k.plan, sq, tile, fb, nb);
+          const int row0 = tile * k.plan.rows;
+          g.head = head;
+          g.seq = seq;
+          g.q0 = sq.q0;
+          g.len = sq.len;
+          g.pos0 = sq.len - sq.n;
+          g.tok0 = row0 / k.plan.group;
+          g.rows = min(k.plan.rows, sq.n * k.plan.group - row0);
+          g.first_key = (fb + blk) * kTBlock;
+          g.todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
+          const int end = row0 + g.rows;
+          g.hi = k.plan.causal ? min(sq.len, g.pos0 + (end - 1) / k.plan.group + 1) : sq.len;
+          g.lo = k.plan.window ? max(0, g.pos0 - k.plan.window + 1) : 0;
+          g.empty = g.hi <= (k.plan.window ? max(0, g.pos0 + g.tok0 - k.plan.window + 1) : 0);
+          g.starts = blk == 0;
+          g.ends = blk + g.todo == nb;
+          if (g.starts && !g.ends) g.last_cta = share_of(st.work, st.used, unit + nb - 1);
+        }
+        const uint32_t i = seg_at % kSegs;
+        if (!wait_all(&seg_empty[i], ((seg_at / kSegs) & 1u) ^ 1u, abort_flag)) break;
+        if (lane == 0) {
+          s_seg[i] = g;
+          mbar_arrive(&seg_full[i]);
+        }
+        __syncwarp();
+        if (more) {
+          left -= g.todo + st.cost;
+          unit += g.todo + st.cost;
+          if (left > 0) {
+            next_tile(k.plan, k.b, head, seq, tile, sq);
+            blk = 0;
+          }
+        }
+      }
+    }
+  } else {
     // ---------------------------------------------------------- weights --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
     const int s = (warp >> 2) - 1, row = tid & (kTRows - 1);
@@ -541,219 +756,6 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tc_fence_after();
       }
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kMmaWarp) {
-      // ----------------------------------------------------------- MMA --
-      // In a step (a block's second product and the first product kStep
-      // blocks on) the streams take turns; issued from a warp each, their
-      // instructions would interleave and both streams' products finish late
-      // (4096 tokens on 12288 keys, 40/8 heads of 128: 670 us for 560).
-      //
-      // The whole warp walks the loop without a branch on what a lane has
-      // seen (wait_soft), and one lane issues: addresses and descriptors are
-      // then the same in all lanes to the compiler too, which keeps them in
-      // the uniform registers that the instructions take.
-      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      constexpr uint32_t kIdS = (1u << 4) | (kType << 7) | (kType << 10) | ((kTBlock >> 3) << 17) | ((kTRows >> 4) << 24);
-      constexpr uint32_t kIdO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kTRows >> 4) << 24);
-      const bool lead = elect_one();
-      const uint64_t qd0 = umma_desc_sw128(q_at), kd0 = umma_desc_sw128(ring_at);
-      const uint64_t vd0 = umma_desc_nmajor(ring_at, C::kHalf);
-      uint32_t pph = 0, qph = 0;   // phases of p_full (a bit per stream) and q_full
-      uint32_t ri = 0, rph = 0;    // ring slot to be consumed next, its phase
-      auto step = [&]() {
-        if (++ri == C::kRing) {
-          ri = 0;
-          rph ^= 1u;
-        }
-      };
-      auto product_s = [&](int s, uint32_t slot) {
-        const uint64_t qd = qd0 + (((PAIR ? s : 0) * C::kTile) >> 4), kd = kd0 + ((slot * C::kTile) >> 4);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * C::kHalf + (ks & 3) * 32u) >> 4;
-          umma_ss(tmem + 128 * s, qd + off, kd + off, kIdS, ks > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[s]);
-      };
-      // Keys in steps of 16, [from, steps) of them.
-      auto product_o = [&](int s, uint32_t slot, int from, int steps, uint32_t keep) {
-        const uint32_t s_col = tmem + 128 * s, o_col = tmem + C::kO + s * D;
-        const uint64_t vd = vd0 + ((slot * C::kTile) >> 4);
-        if (from == 0 && steps == kTBlock / 16) {
-#pragma unroll
-          for (int ks = 0; ks < kTBlock / 16; ++ks)
-            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > 0 ? 1u : keep);
-        } else {
-          for (int ks = from; ks < steps; ++ks)
-            umma_ts(o_col, s_col + 8 * ks, vd + ((ks * 2048u) >> 4), kIdO, ks > from ? 1u : keep);
-        }
-      };
-      for (uint32_t at = 0;; ++at) {
-        wait_soft(&seg_full[at % kSegs], (at / kSegs) & 1u, &s_abort);
-        const int n = uniform(*abort_flag ? 0 : s_seg[at % kSegs].todo), none = uniform(s_seg[at % kSegs].empty);
-        const int first_key = uniform(s_seg[at % kSegs].first_key), hi = uniform(s_seg[at % kSegs].hi);
-        const int lo = uniform(s_seg[at % kSegs].lo);
-        if (lead) mbar_arrive(&seg_empty[at % kSegs]);
-        if (n == 0) break;
-        if (none) continue;
-        wait_soft(&q_full, qph, &s_abort);
-        qph ^= 1u;
-#pragma unroll
-        for (int i = 0; i < C::kStep; ++i) {
-          if (i >= n) break;
-          wait_soft(&full[ri], rph, &s_abort);
-          tc_fence_after();
-          if (lead) {
-            product_s(PAIR ? 0 : i, ri);
-            if (PAIR) product_s(1, ri);
-            umma_commit(&empty[ri]);
-          }
-          step();
-        }
-        for (int i = 0; i < n; ++i) {
-          const bool more = i + C::kStep < n;
-          // The last first product is on its way.
-          if (lead && (i + C::kStep == n || (i == 0 && n < C::kStep))) umma_commit(&q_empty);
-          const int key0 = first_key + i * kTBlock;
-          const int steps = (min(kTBlock, hi - key0) + 15) >> 4, from = max(0, lo - key0) >> 4;
-          const uint32_t slot = ri, sph = rph;
-          step();
-          const uint32_t nslot = ri, nph = rph;
-          if (more) step();
-          wait_soft(&full[slot], sph, &s_abort);
-          if (more) wait_soft(&full[nslot], nph, &s_abort);
-#pragma unroll
-          for (int u = 0; u < (PAIR ? 2 : 1); ++u) {
-            const int s = PAIR ? u : (i & 1);
-            wait_soft(&p_full[s], (pph >> s) & 1u, &s_abort);
-            pph ^= 1u << s;
-            tc_fence_after();
-            if (lead) {
-              product_o(s, slot, from, steps, i >= C::kStep ? 1u : 0u);
-              if (u == (PAIR ? 1 : 0)) umma_commit(&empty[slot]);
-              if (more) {
-                product_s(s, nslot);
-                if (u == (PAIR ? 1 : 0)) umma_commit(&empty[nslot]);
-              } else {
-                umma_commit(&o_full[s]);
-              }
-            }
-          }
-        }
-      }
-      // After an abort, let the products already issued finish (bounded).
-      __syncwarp();
-      if (*abort_flag) {
-        if (lead) umma_commit(&drained);
-        (void)mbar_wait(&drained, 0);
-      }
-    } else if (warp == kLoadWarp) {
-      // --------------------------------------------------------- copies --
-      uint32_t at = 0, segs = 0;  // ring slots filled, segments read
-      bool ok = true;
-      const int boxes = kTBlock / k.box_keys;  // of a block
-      const int half = lane & (D / 64 - 1), box = lane / (D / 64);
-      // The page of this lane's box of the block from key0 on: -1 (read as
-      // zeros) where the table names none, -2 past the sequence's end.
-      auto page_of = [&](int key0) {
-        const int key = key0 + box * k.box_keys;
-        if (box >= boxes || key >= g.len) return -2;
-        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
-        if (id >= 0 && id < k.c.n_pages) return id;
-        raise_status(k.status, kStatusBadId);
-        return -1;
-      };
-      auto copy = [&](const CUtensorMap* map, int key0, int page) {
-        const uint32_t slot = at % C::kRing;
-        if (!(ok = wait_all(&empty[slot], ((at / C::kRing) & 1u) ^ 1u, abort_flag))) return false;
-        const uint32_t live = __ballot_sync(0xffffffffu, page != -2);
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], __popc(live) * k.box_keys * 128);
-        __syncwarp();
-        if (page != -2)
-          tma_load_4d(ring_at + slot * C::kTile + half * C::kHalf + box * k.box_keys * 128, map, 64 * half,
-                      (key0 + box * k.box_keys) & (k.c.page_size - 1), g.head, page, &full[slot]);
-        ++at;
-        return true;
-      };
-      while (ok && next_segment() && g.todo > 0) {
-        if (g.empty) continue;
-        int page[C::kStep];
-#pragma unroll
-        for (int i = 0; i < C::kStep; ++i) page[i] = i < g.todo ? page_of(g.first_key + i * kTBlock) : -2;
-        if (!(ok = wait_all(&q_empty, (segs & 1u) ^ 1u, abort_flag))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&q_full, C::kQTiles * (D / 64) * k.stream_rows * 128);
-        __syncwarp();
-        if (lane < C::kQTiles * (D / 64)) {
-          const int qs = lane / (D / 64), qhalf = lane & (D / 64 - 1);
-          tma_load_3d(q_at + qs * C::kTile + qhalf * C::kHalf, &tmq, 64 * qhalf, g.head * k.plan.group,
-                      g.q0 + g.tok0 + qs * k.stream_tokens, &q_full);
-        }
-        ++segs;
-        for (int i = 0; i < C::kStep && i < g.todo && ok; ++i) copy(&tmk, g.first_key + i * kTBlock, page[i]);
-        for (int i = 0; i < g.todo && ok; ++i) {
-          const int next = i + C::kStep, key = g.first_key + i * kTBlock;
-          const int np = next < g.todo ? page_of(g.first_key + next * kTBlock) : -2;
-          if (!copy(&tmv, key, page[0])) break;
-          if (next < g.todo && !copy(&tmk, g.first_key + next * kTBlock, np)) break;
-#pragma unroll
-          for (int j = 0; j + 1 < C::kStep; ++j) page[j] = page[j + 1];
-          page[C::kStep - 1] = np;
-        }
-      }
-      // Copies still in flight must land before the CTA leaves.
-      if (lane == 0 && *abort_flag) {
-        for (uint32_t i = at > C::kRing ? at - C::kRing : 0; i < at; ++i)
-          (void)mbar_wait(&full[i % C::kRing], (i / C::kRing) & 1u);
-        if (segs) (void)mbar_wait(&q_full, (segs - 1) & 1u);
-      }
-    } else if (warp == kPlanWarp) {
-      // ----------------------------------------------------------- plan --
-      int head = st.head, seq = st.seq, tile = st.tile, blk = st.block;
-      int64_t left = st.units, unit = st.first;
-      Seq sq = st.sq;
-      for (bool more = true; more; ++seg_at) {
-        g = Segment{};
-        more = left > 0;
-        if (more) {
-          int fb, nb;
-          tile_blocks(k.plan, sq, tile, fb, nb);
-          const int row0 = tile * k.plan.rows;
-          g.head = head;
-          g.seq = seq;
-          g.q0 = sq.q0;
-          g.len = sq.len;
-          g.pos0 = sq.len - sq.n;
-          g.tok0 = row0 / k.plan.group;
-          g.rows = min(k.plan.rows, sq.n * k.plan.group - row0);
-          g.first_key = (fb + blk) * kTBlock;
-          g.todo = static_cast<int>(min(static_cast<int64_t>(nb - blk), left));
-          const int end = row0 + g.rows;
-          g.hi = k.plan.causal ? min(sq.len, g.pos0 + (end - 1) / k.plan.group + 1) : sq.len;
-          g.lo = k.plan.window ? max(0, g.pos0 - k.plan.window + 1) : 0;
-          g.empty = g.hi <= (k.plan.window ? max(0, g.pos0 + g.tok0 - k.plan.window + 1) : 0);
-          g.starts = blk == 0;
-          g.ends = blk + g.todo == nb;
-          if (g.starts && !g.ends) g.last_cta = share_of(st.work, st.used, unit + nb - 1);
-        }
-        const uint32_t i = seg_at % kSegs;
-        if (!wait_all(&seg_empty[i], ((seg_at / kSegs) & 1u) ^ 1u, abort_flag)) break;
-        if (lane == 0) {
-          s_seg[i] = g;
-          mbar_arrive(&seg_full[i]);
-        }
-        __syncwarp();
-        if (more) {
-          left -= g.todo + st.cost;
-          unit += g.todo + st.cost;
-          if (left > 0) {
-            next_tile(k.plan, k.b, head, seq, tile, sq);
-            blk = 0;
-          }
-        }
-      }
-    }
   }
   __syncthreads();
   if (tid == 0 && *abort_flag) raise_status(k.status, kStatusTimeout);
@@ -817,7 +819,7 @@ int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool
   k.c = c;
   k.b = b;
   k.a = a;
-  k.plan = {attn_tile_rows(group, pair), group, a.causal, a.window, kTShift};
+  k.plan = {Divisor(attn_tile_rows(group, pair)), Divisor(group), a.causal, a.window, kTShift};
   k.parts = parts;
   k.slots = slots;
   k.status = status;
