@@ -452,10 +452,10 @@ namespace {
 // of an average sequence: kWarps for up to one 16-row tile, else the 128-row
 // kernel, with two such tiles side by side where one does not hold them.
 // Measured, 32 sequences of 2000 keys, 32/8 heads of 128 (of 64), us:
-//   rows        4           16           20            128           136
-//   kWarps      50 (30)     53 (33)      101 (62)      326 (181)     366 (200)
-//   kTile       52 (37)     53 (37)      53 (38)       64 (41)       112 (75)
-//   kTilePair   56 (47)     57 (48)      57 (48)       68 (50)       70 (51)
+//   rows        4           16           20           128           136
+//   kWarps      48 (30)     51 (32)      97 (58)      322 (173)     359 (191)
+//   kTile       51 (37)     52 (38)      52 (38)      61 (40)       108 (72)
+//   kTilePair   56 (48)     58 (49)      58 (49)      66 (51)       66 (51)
 enum Route { kWarps, kTile, kTilePair };
 Route route(int64_t t, int64_t group, int64_t n_seqs) {
   const int64_t rows = (t * group + n_seqs - 1) / n_seqs;
