@@ -57,7 +57,8 @@ inline PagesWs split_ws(void* ws, int64_t n_pages) {
   return w;
 }
 
-__device__ __forceinline__ int up(int a, int b) { return (a + b - 1) / b; }
+// Pages of `a` slots; any length up to the type's largest.
+__device__ __forceinline__ int up(int a, int b) { return a > 0 ? (a - 1) / b + 1 : 0; }
 
 // This thread's four counts of the chunk of pages from `base` on; pages past
 // the end are in use.

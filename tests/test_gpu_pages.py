@@ -71,6 +71,14 @@ def test_no_pages_left():
     b.check()
 
 
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 15, 2 ** 31 - 16, 2 ** 30 + 1])
+def test_lengths_that_no_row_holds(length):
+    b = Both(3, 8, 12)
+    b.resize([0, 1], [20, 5])
+    b.resize([1, 0, 2], [length, 33, 16])
+    b.check()
+
+
 def test_fork_shares_and_copies():
     b = Both(8, 6, 24)
     b.resize([0, 1, 2], [40, 32, 5])
