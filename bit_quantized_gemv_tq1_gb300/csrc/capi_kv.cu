@@ -87,7 +87,7 @@ int get_pool(const tq1_page_pool* p, PagePool* out) {
   out->n_pages = static_cast<int>(p->n_pages);
   out->n_seqs = static_cast<int>(p->n_seqs);
   out->max_pages = static_cast<int>(p->max_pages);
-  out->page_size = static_cast<int>(p->page_size);
+  out->page_size = Divisor(static_cast<int>(p->page_size));
   return TQ1_OK;
 }
 

@@ -57,25 +57,6 @@ __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
   return r;
 }
 
-// A divisor of non-negative 32-bit integers that the host knows, with its
-// reciprocal (Granlund and Montgomery, 1994): n / d = (hi(n mul) + n) >> shift
-// with 2^shift >= d > 2^(shift - 1) and mul = floor(2^32 (2^shift - d) / d) + 1.
-// The search for a CTA's first unit stands before everything else of a call;
-// the compiler's divisions were the larger part of its instructions.
-struct Divisor {
-  int d, shift;
-  uint32_t mul;
-  Divisor() = default;
-  explicit Divisor(int v) : d(v), shift(0) {
-    while ((int64_t{1} << shift) < v) ++shift;
-    mul = static_cast<uint32_t>((((uint64_t{1} << shift) - static_cast<uint64_t>(v)) << 32) / static_cast<uint64_t>(v)) + 1;
-  }
-  __host__ __device__ __forceinline__ operator int() const { return d; }
-};
-__device__ __forceinline__ int operator/(int n, const Divisor& v) {
-  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), v.mul) + static_cast<uint32_t>(n)) >> v.shift);
-}
-
 // ------------------------------------------------- division of attention --
 // The (token, query head of the group) pairs of one sequence and one kv head
 // are its rows, row = token * group + head, cut into tiles of `rows` rows.

@@ -18,6 +18,28 @@ enum : unsigned { kStatusNoPages = 4u };
 // nullptr when a runtime call failed.
 unsigned* status_word();
 
+// A divisor of non-negative 32-bit integers that the host knows, with its
+// reciprocal (Granlund and Montgomery, 1994): n / d = (hi(n mul) + n) >> shift
+// with 2^shift >= d > 2^(shift - 1) and mul = floor(2^32 (2^shift - d) / d) + 1.
+// What a kernel computes before its first loads or between those that follow
+// one another is as long as its instructions, and the compiler's divisions were
+// the larger part of them.
+struct Divisor {
+  int d, shift;
+  uint32_t mul;
+  Divisor() = default;
+  explicit Divisor(int v) : d(v), shift(0) {
+    while ((int64_t{1} << shift) < v) ++shift;
+    mul = static_cast<uint32_t>((((uint64_t{1} << shift) - static_cast<uint64_t>(v)) << 32) / static_cast<uint64_t>(v)) + 1;
+  }
+  __host__ __device__ __forceinline__ operator int() const { return d; }
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ int operator/(int n, const Divisor& v) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), v.mul) + static_cast<uint32_t>(n)) >> v.shift);
+}
+#endif
+
 struct KvCache {
   uint16_t *k, *v;                                 // 16-bit elements
   int64_t page_stride, head_stride, slot_stride;   // elements
@@ -69,7 +91,8 @@ struct PagePool {
   uint8_t* base;
   int64_t pool_stride, page_bytes;
   int32_t *table, *kv_len, *refs;
-  int n_pools, n_pages, n_seqs, max_pages, page_size;
+  int n_pools, n_pages, n_seqs, max_pages;
+  Divisor page_size;
 };
 
 size_t pages_workspace_bytes(int64_t n_pages, int64_t n_seqs);

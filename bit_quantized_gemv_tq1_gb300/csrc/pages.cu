@@ -58,7 +58,9 @@ inline PagesWs split_ws(void* ws, int64_t n_pages) {
 }
 
 // Pages of `a` slots; any length up to the type's largest.
-__device__ __forceinline__ int up(int a, int b) { return a > 0 ? (a - 1) / b + 1 : 0; }
+__device__ __forceinline__ int up(int a, const Divisor& b) { return a > 0 ? (a - 1) / b + 1 : 0; }
+// Whether the last page of `a` > 0 slots is filled in part only.
+__device__ __forceinline__ bool partly(int a, const Divisor& b) { return a / b * b.d != a; }
 
 // This thread's four counts of the chunk of pages from `base` on; pages past
 // the end are in use.
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const PagePool p, 
           s = -1;
           had = 0;
         } else {
-          if (want > len && len % p.page_size != 0) last = p.table[static_cast<int64_t>(s) * p.max_pages + had - 1];
+          if (want > len && partly(len, p.page_size)) last = p.table[static_cast<int64_t>(s) * p.max_pages + had - 1];
           keep = min(had, up(want, p.page_size));
           if (want <= len) p.kv_len[s] = want;
         }
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(const PagePool p, 
         } else {
           len = max(p.kv_len[s], 0);
           if (want < 0 || up(want, p.page_size) > p.max_pages || up(len, p.page_size) > p.max_pages) s = -1;
-          if (s >= 0 && want > len && len % p.page_size != 0)
+          if (s >= 0 && want > len && partly(len, p.page_size))
             last = p.table[static_cast<int64_t>(s) * p.max_pages + up(len, p.page_size) - 1];
         }
       }
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_kernel(const PagePool p, co
       }
     }
     const int full = s >= 0 ? len / p.page_size : 0;
-    const bool part = s >= 0 && len % p.page_size != 0;
+    const bool part = s >= 0 && partly(len, p.page_size);
     const int64_t from = static_cast<int64_t>(max(s, 0)) * p.max_pages, to = static_cast<int64_t>(max(c, 0)) * p.max_pages;
     const int last = part ? p.table[from + full] : -1;
     int total;
