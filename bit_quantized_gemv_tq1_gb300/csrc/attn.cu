@@ -23,6 +23,7 @@
 // SM); one of 777: 8 us, the latency of two launches.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/tq1.h"
 #include "kv.cuh"
@@ -89,6 +90,15 @@ __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&c)[4], const uint32
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// log2 of what the weights are formed times, so that their 16-bit form spans
+// as much below the largest as the type can hold: it cancels in O / l.  In
+// fp16, weights from 1 down would be subnormal below 2^-14 and zero below
+// 2^-25, while l counts them (4000 keys with weights of e^-17 to e^-20 behind
+// 16 of weight 1: an output that is theirs came out 10 to 16% small); times
+// 2^15 they are whole down to 2^-29.  bf16 has fp32's range.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 15.0f : 0.0f;
 
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -273,13 +283,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const float mx = quad_max(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
         const float mn = fmaxf(m[h], mx);
         const float base_m = mn == -INFINITY ? 0.0f : mn;  // no key seen yet: every weight below is exp2(-inf) = 0
-        const float keep = exp2f(m[h] - base_m);
+        const float keep = exp2f(m[h] - base_m), top = base_m - kLift<T>;
         m[h] = mn;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = exp2f(x[j] - base_m);
+        for (int j = 0; j < 4; ++j) x[j] = exp2f(x[j] - top);
         l[h] = l[h] * keep + ((x[0] + x[1]) + (x[2] + x[3]));
-        // The weights enter the second product as 16-bit numbers in [0, 1]
-        // (the type the matrix instruction pairs with V's); the sum stays fp32.
+        // The weights enter the second product as 16-bit numbers (the type
+        // the matrix instruction pairs with V's); the sum stays fp32.  A
+        // second number for the rest of each would take as many instructions
+        // again (200 sequences' step, fp16, d = 128: 90 us so, 99 with it).
         p[h] = pack2<T>(x[0], x[1]);
         p[2 + h] = pack2<T>(x[2], x[3]);
         if (__any_sync(0xffffffffu, keep != 1.0f)) {

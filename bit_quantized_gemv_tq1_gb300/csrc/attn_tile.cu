@@ -46,6 +46,7 @@
 // Every wait is bounded; the first that runs out sets an abort flag that
 // releases the others, and TQ1_ERR_TIMEOUT is raised.
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/tq1.h"
 #include "kv.cuh"
@@ -62,6 +63,13 @@ constexpr int kWeightRegs = 208, kOtherRegs = 88;
 constexpr int kTRows = 128;   // rows of a stream (tensor-memory lanes)
 constexpr int kTShift = 7, kTBlock = 1 << kTShift;  // keys of a block
 constexpr float kMoveAt = 8.0f;  // log2 of how far a row's maximum may outgrow its reference
+// log2 of what the weights are formed times (it cancels in O / l): with it the
+// largest weight there can be, 2^kMoveAt of the reference's, is 2^15, which
+// fp16 just holds; so weights down to 2^-21 of the reference's are whole and
+// nothing is zero above 2^-32, where without it those are 2^-14 and 2^-25.
+// bf16 has fp32's range.
+template <typename T>
+constexpr float kTLift = std::is_same<T, __half>::value ? 15.0f - kMoveAt : 0.0f;
 
 template <int D, bool PAIR>
 struct TileCfg {
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
               }
             }
           }
-          const float base = m == -INFINITY ? 0.0f : -m * sc;  // no key seen yet: all weights are exp2(-inf) = 0
+          const float base = m == -INFINITY ? 0.0f : kTLift<T> - m * sc;  // no key seen yet: all weights are exp2(-inf) = 0
           float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

@@ -1,0 +1,63 @@
+"""tq1_paged_attn at the edges of its numbers, masks, tables and workspaces."""
+import math
+
+import pytest
+import torch
+
+from . import kv_ref
+from .gpu_util import lib
+from .kv_ref import Batch, attention, rounded
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def attend(b, q, n_q, scale, out_dtype=None, window=0, causal=True, ws=None):
+    L = lib()
+    out = torch.full((b.t, n_q, b.d), 7.0, dtype=out_dtype or b.dtype, device="cuda")
+    if ws is None:
+        ws = torch.empty(L.tq1_paged_attn_workspace_size(b.cache, b.t, n_q, len(b.new)), dtype=torch.uint8, device="cuda")
+    L.tq1_paged_attn(b.cache, b.batch, q, out, scale, causal=causal, window=window, ws=ws)
+    return out
+
+
+def queries(b, n_q):
+    q = torch.randn(b.t, n_q, b.d, generator=b.g).to(b.dtype)
+    return q, q.cuda()
+
+
+@pytest.mark.parametrize("new,lift", [(1, 15), (5, 15), (40, 7), (200, 7)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_beside_large_ones(new, lift, d):
+    # Sixteen keys with the largest weight and values of zero, one in every 16
+    # of the first 256; 3744 others with weights of e^-17 to e^-20 of that,
+    # below fp16's smallest number, whose values make up the output.  Weights
+    # are formed times 2^lift: half the spacing of fp16's smallest numbers is
+    # then 2^(-25-lift) of the largest weight.  As many heads and sequences as
+    # let every CTA have long runs of keys behind the large ones.
+    L, n, heads, seqs = lib(), 4000, 8, 20
+    b = Batch([new], [n], 32, heads, d, F16, seed=new)
+    pages = b.table[0, :n // 32].long()
+    x = -17 - torch.randint(0, 193, (n,), generator=b.g) / 64
+    x[5:256:16] = 0
+    x = x.to(F16)
+    b.kv[0] = 0
+    b.kv[0, pages, :, :, 0] = x.view(-1, 1, 32)
+    b.kv[1] = b.kv[1].abs() + 0.5
+    for j in range(5, 256, 16):
+        b.kv[1, pages[j // 32], :, j % 32] = 0
+    b.to_gpu(L)
+    b.t *= seqs
+    b.new = [new] * seqs
+    b.gtable, b.glen = b.gtable.repeat(seqs, 1), b.glen.repeat(seqs)  # all read the same pages
+    b.gq = torch.arange(0, b.t + 1, new, dtype=torch.int32, device="cuda")
+    b.batch = L.tq1_kv_batch(b.gtable, b.gq, b.glen)
+    q = torch.zeros(b.t, heads, d, dtype=F16, device="cuda")
+    q[..., 0] = 1
+    out = attend(b, q, heads, 1.0, F32, causal=False).cpu().double()
+    assert L.tq1_sync_status() == 0
+    e, v = x.double().exp(), b.sequence(0, 1)
+    want = (e[:, None, None] * v).sum(0) / e.sum()  # every term is positive
+    tol = want * (kv_ref.UNIT[F16] + 2.0 ** -20 + 2 * n * 2.0 ** -24) + n * 2.0 ** (-25 - lift) * v.max() / e.sum()
+    assert ((out - want).abs() <= tol).all(), float(((out - want).abs() / tol).max())
