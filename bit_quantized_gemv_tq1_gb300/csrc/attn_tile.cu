@@ -434,10 +434,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const int boxes = kTBlock / k.box_keys;  // of a block
       const int half = lane & (D / 64 - 1), box = lane / (D / 64);
       // The page of this lane's box of the block from key0 on: -1 (read as
-      // zeros) where the table names none, -2 past the sequence's end.
+      // zeros) where the table names none, -2 past the sequence's end and
+      // before the window of its first token (whose page may be gone): not
+      // read, as no row of the call sees it.
       auto page_of = [&](int key0) {
         const int key = key0 + box * k.box_keys;
-        if (box >= boxes || key >= g.len) return -2;
+        if (box >= boxes || key >= g.len || key + k.box_keys <= g.lo) return -2;
         const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
         if (id >= 0 && id < k.c.n_pages) return id;
         raise_status(k.status, kStatusBadId);

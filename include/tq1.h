@@ -520,10 +520,11 @@ size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64
  * Scores, maxima, sums and outputs are accumulated in fp32; the weights p
  * enter the second product as 16-bit numbers of the cache's type.  Slots at
  * or past kv_len, and slots before the window of a sequence's first new token,
- * may hold anything, NaN included.  Keys that are not finite hurt only the
- * rows that see them; values that are not finite, in a chunk of several
- * tokens, also rows of nearby tokens that do not see them (a weight of zero
- * does not silence them).
+ * may hold anything, NaN included, and the table entries of pages that have no
+ * other slots are not read (a cache may free what its window has passed).
+ * Keys that are not finite hurt only the rows that see them; values that are
+ * not finite, in a chunk of several tokens, also rows of nearby tokens that do
+ * not see them (a weight of zero does not silence them).
  * Deterministic.  head_dim 64 or 128, n_q a multiple of n_kv, at most 128
  * query heads per kv head, t * n_q / n_kv <= 2^30 (TQ1_ERR_UNSUPPORTED
  * otherwise); scale > 0; ldq, ldo multiples of 8.

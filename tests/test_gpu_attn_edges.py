@@ -61,3 +61,22 @@ def test_many_small_weights_beside_large_ones(new, lift, d):
     want = (e[:, None, None] * v).sum(0) / e.sum()  # every term is positive
     tol = want * (kv_ref.UNIT[F16] + 2.0 ** -20 + 2 * n * 2.0 ** -24) + n * 2.0 ** (-25 - lift) * v.max() / e.sum()
     assert ((out - want).abs() <= tol).all(), float(((out - want).abs() / tol).max())
+
+
+@pytest.mark.parametrize("window", [1, 16, 100, 333])
+@pytest.mark.parametrize("new", [1, 3, 40, 260])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 16), (128, 64)])
+def test_pages_before_the_window_may_be_gone(d, page, window, new):
+    # A cache that frees what its window has passed: the table names no page
+    # there (or one that is no page any more), and that is no error.
+    length = [new + 399, new + 2001]
+    b = Batch([new, new], length, page, 2, d, F16, seed=window).to_gpu(lib())
+    q, gq = queries(b, 6)
+    for i, ln in enumerate(length):
+        gone = max(0, ln - new + 1 - window) // page
+        b.gtable[i, :gone] = -1
+        b.gtable[i, :gone:3] = b.n_pages + 7
+    out = attend(b, gq, 6, 0.125, window=window)
+    assert lib().tq1_sync_status() == 0
+    want, tol = attention(b, q, 0.125, True, window)
+    assert ((out.cpu().double() - want).abs() <= rounded(tol, want, F16)).all()
