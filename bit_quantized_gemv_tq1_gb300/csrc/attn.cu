@@ -353,8 +353,11 @@ __global__ void __launch_bounds__(kAThreads, 1)
           v.z += f * x.z;
           v.w += f * x.w;
         }
+        // A row that sees nothing here is zero, whatever the values are that
+        // other rows see (its weights of zero did not silence a NaN).
+        if (lt == 0.0f) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (whole) {
-          const float inv = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);  // a row that sees nothing is zero
+          const float inv = lt > 0.0f ? 1.0f / lt : (lt == 0.0f ? 0.0f : lt);
           const int tok = (row0 + r) / plan.group, qh = cur.head * plan.group + (row0 + r) - tok * plan.group;
           store4<T>(a, cur.sq.q0 + tok, qh, D, col, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         } else {

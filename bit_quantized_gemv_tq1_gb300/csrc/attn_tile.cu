@@ -678,9 +678,11 @@ __global__ void __launch_bounds__(kTThreads, 1)
         tc_fence_after();
       }
       // Out: the row over its sum, or, of a tile that others share, the row
-      // as it is.  Two streams on one tile first tell each other their m and
-      // l; then each does half the columns of both.
-      float mrow = m == -INFINITY ? m : m * sc, lrow = l, f0 = 1.0f, f1 = 0.0f;
+      // as it is; zero where it sees nothing, whatever the values are that
+      // other rows see (its weights of zero did not silence a NaN).  Two
+      // streams on one tile first tell each other their m and l; then each
+      // does half the columns of both.
+      float mrow = m == -INFINITY ? m : m * sc, lrow = l, f0 = l == 0.0f ? 0.0f : 1.0f, f1 = 0.0f;
       if (!PAIR) {
         s_ml[s][0][row] = mrow;
         s_ml[s][1][row] = l;
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const bool whole = g.starts && g.ends;
       const int slot = first_seg ? 2 * cta : 2 * cta + 1;
       float* out = k.slots + slot * join_slot_floats(k.plan.rows, D);
-      const float inv = lrow > 0.0f ? 1.0f / lrow : (lrow == 0.0f ? 0.0f : lrow);  // a row that sees nothing is zero
+      const float inv = lrow > 0.0f ? 1.0f / lrow : (lrow == 0.0f ? 0.0f : lrow);
       const int64_t at = static_cast<int64_t>(g.q0 + tok) * k.a.ldo + static_cast<int64_t>(qh) * D;
       constexpr int kCols = PAIR ? D : D / 2;
 #pragma unroll 1

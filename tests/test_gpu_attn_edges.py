@@ -80,3 +80,23 @@ def test_pages_before_the_window_may_be_gone(d, page, window, new):
     assert lib().tq1_sync_status() == 0
     want, tol = attention(b, q, 0.125, True, window)
     assert ((out.cpu().double() - want).abs() <= rounded(tol, want, F16)).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("new,length,n_q", [([4], [2], 2), ([9, 1, 5], [8, 3, 1], 2), ([50], [30], 2), ([150], [100], 4),
+                                            ([700, 1], [600, 40], 4), ([2600], [2500], 6), ([12] * 40, [7] * 40, 2)])
+def test_rows_that_see_nothing_are_zero_whatever_the_values_are(new, length, n_q, f32, bad):
+    # More new tokens than slots: the first rows stand before the first slot.
+    b = Batch(new, length, 16, 2, 64, F16)
+    b.kv[1] = bad
+    b.to_gpu(lib())
+    _, gq = queries(b, n_q)
+    out = attend(b, gq, n_q, 0.125, F32 if f32 else None).cpu()
+    assert lib().tq1_sync_status() == 0
+    at = 0
+    for n, ln in zip(new, length):
+        none = max(n - ln, 0)
+        assert (out[at:at + none] == 0).all()
+        assert not out[at + none:at + n].isfinite().any()
+        at += n
