@@ -539,6 +539,9 @@ int launch_route(Route r, const KvCache& c, const KvBatch& b, const AttnArgs& a,
 
 }  // namespace
 
+// What a call of exactly these sizes needs: fewer bytes where more sequences
+// share the tokens (64 tokens, group 4, d = 128: 2.5 MB of 64 sequences, 40 MB
+// of one).
 size_t attn_workspace_bytes(const KvCache& c, int64_t t, int64_t n_q, int64_t n_seqs) {
   const int group = static_cast<int>(n_q / c.n_kv);
   if (group < 1 || group > 128) return 0;

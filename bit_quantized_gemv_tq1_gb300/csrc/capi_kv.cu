@@ -151,7 +151,9 @@ size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64
   KvCache c;
   if (get_cache(cache, &c) != TQ1_OK || t < 0 || n_q <= 0 || n_q > 65536 || n_seqs <= 0 || t > (int64_t{1} << 24)) return 0;
   if (!status_word()) return 0;
-  return attn_workspace_bytes(c, t, n_q, n_seqs);
+  // One sequence has the widest tiles: what its call needs grows with t and
+  // serves t tokens of any number of sequences.
+  return attn_workspace_bytes(c, t, n_q, 1);
 }
 
 int tq1_paged_attn(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const void* q, int64_t ldq, int64_t t,

@@ -499,9 +499,11 @@ int tq1_rope_append(const tq1_kv_cache* cache, const tq1_kv_batch* batch, const 
                     const float* inv_freq, int64_t rot_dim, int interleaved, float mscale, const int32_t* positions,
                     void* stream);
 
-/* Workspace bytes tq1_paged_attn needs for t tokens of n_seqs sequences with
- * n_q query heads (0: invalid arguments).  No passage: a convention of this
- * library. */
+/* Workspace bytes for tq1_paged_attn on t tokens of n_seqs sequences with n_q
+ * query heads (0: invalid arguments).  What t tokens need depends on how they
+ * are spread over sequences; the bytes returned serve any spread, and fewer
+ * tokens too: a workspace for a server's largest t serves all its batches.
+ * No passage: a convention of this library. */
 size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64_t n_q, int64_t n_seqs);
 
 /*

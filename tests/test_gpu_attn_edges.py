@@ -100,3 +100,19 @@ def test_rows_that_see_nothing_are_zero_whatever_the_values_are(new, length, n_q
         assert (out[at:at + none] == 0).all()
         assert not out[at + none:at + n].isfinite().any()
         at += n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_q,n_kv", [(8, 2), (1, 1), (96, 1)])
+def test_a_workspace_for_the_largest_batch_serves_smaller_ones(d, n_q, n_kv):
+    L = lib()
+    most = Batch([1] * 64, [40] * 64, 16, n_kv, d, F16).to_gpu(L)
+    ws = torch.empty(L.tq1_paged_attn_workspace_size(most.cache, 64, n_q, 64), dtype=torch.uint8, device="cuda")
+    for new in ([64], [63, 1], [1] * 64, [7] * 9, [2], [33] + [0] * 40 + [31], [16, 16, 16, 16]):
+        b = Batch(new, [n + 50 for n in new], 16, n_kv, d, F16, seed=len(new)).to_gpu(L)
+        assert L.tq1_paged_attn_workspace_size(b.cache, b.t, n_q, len(new)) <= ws.numel()
+        q, gq = queries(b, n_q)
+        out = attend(b, gq, n_q, 0.125, ws=ws)
+        assert L.tq1_sync_status() == 0
+        want, tol = attention(b, q, 0.125, True, 0)
+        assert ((out.cpu().double() - want).abs() <= rounded(tol, want, F16)).all()
