@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   const Start st = find_start<kAThreads>(plan, b, c.n_kv, cta, ctas, reinterpret_cast<int64_t*>(smem));
   __syncthreads();
   if (tid < 2) parts[2 * cta + tid].rows = 0;
+  if (st.bad && cta == 0 && tid == 0) raise_status(status, kStatusBadId);
   if (st.units == 0) return;
   __syncthreads();
 

@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the copies below write where the search wrote
   __syncthreads();
   if (tid < 2) k.parts[2 * cta + tid].rows = 0;
+  if (st.bad && cta == 0 && tid == 0) raise_status(k.status, kStatusBadId);
   __syncthreads();
   // The next segment, for one of the reading warps; false after an abort.
   uint32_t seg_at = 0;

@@ -141,6 +141,7 @@ struct Start {
   int64_t work;                // units of the call
   int used;                    // CTAs that have some
   int cost;                    // units of a tile beside its blocks
+  bool bad;                    // starts that do not ascend: there is no work
   Seq sq;                      // of `seq`
 };
 
@@ -168,6 +169,12 @@ template <int NT>
 __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b, int n_kv, int cta, int ctas, int64_t* s_nb) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int* const s_nt = reinterpret_cast<int*>(s_nb + b.n_seqs);
+  // Sequences that share no token have at most this many tiles (2^26 + 2^13).
+  // Starts that do not ascend can make them share tokens, up to n_seqs times
+  // as many; all the counts below rely on this limit, so such a call is
+  // refused, and no warp counts the blocks of more tiles than that.
+  const int most = b.t * p.group / p.rows + b.n_seqs;
+  int counted = 0;
   // Blocks and tiles of each sequence: by its thread where it has one tile, else (left
   // as -1) by a warp, a lane per tile.
   for (int s0 = 32 * warp; s0 < b.n_seqs; s0 += NT) {
@@ -188,7 +195,8 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
       const Seq q = load_seq(b, t);
       const int tiles = seq_tiles(p, q);
       int64_t sum = 0;
-      for (int i = lane; i < tiles; i += 32) {
+      counted = min(counted + tiles, most + 1);
+      for (int i = lane; i < tiles && counted <= most; i += 32) {
         int f, c;
         tile_blocks(p, q, i, f, c);
         sum += c;
@@ -201,21 +209,22 @@ __device__ __forceinline__ Start find_start(const TilePlan& p, const KvBatch& b,
   // A lane per run of sequences: their sum, the sum of all, and the lane
   // whose run holds the first unit.
   const int run = (b.n_seqs + 31) >> 5, s0 = lane * run, s1 = min(s0 + run, b.n_seqs);
-  int64_t mine = 0;
-  int mine_t = 0;
+  int64_t mine = 0, many = 0;
   for (int s = s0; s < s1; ++s) {
     mine += s_nb[s];
-    mine_t += s_nt[s];
+    many += s_nt[s];
   }
   int64_t end = warp_scan(mine);
-  const int end_t = warp_scan(mine_t);
+  const uint32_t mine_t = static_cast<uint32_t>(min(many, int64_t{most} + 1));
+  const uint32_t end_t = warp_scan(mine_t), all_t = __shfl_sync(0xffffffffu, end_t, 31);  // 32 (most + 1) < 2^32
   int64_t all = __shfl_sync(0xffffffffu, end, 31);  // blocks of one kv head
   Start r;
-  r.cost = all * n_kv < static_cast<int64_t>(kTileCost) * ctas ? kTileCost - 1 : kTileCost;
+  r.bad = all_t > static_cast<uint32_t>(most);
+  r.cost = !r.bad && all * n_kv < static_cast<int64_t>(kTileCost) * ctas ? kTileCost - 1 : kTileCost;
   mine += static_cast<int64_t>(r.cost) * mine_t;
   end += static_cast<int64_t>(r.cost) * end_t;
-  all += static_cast<int64_t>(r.cost) * __shfl_sync(0xffffffffu, end_t, 31);  // units of one kv head
-  const int64_t work = all * n_kv;
+  all += static_cast<int64_t>(r.cost) * all_t;  // units of one kv head
+  const int64_t work = r.bad ? 0 : all * n_kv;
   const int used = static_cast<int>(min(work, static_cast<int64_t>(ctas)));  // fewer units than CTAs: one each
   r.work = work;
   r.used = used;

@@ -441,7 +441,8 @@ typedef struct tq1_kv_cache {
  * q_start[s + 1] - 1 (none is fine) and kv_len[s] tokens in all, these
  * included; so its token i stands at position kv_len[s] - (q_start[s + 1] -
  * i).  Tokens from q_start[n_seqs] on belong to no sequence and are left
- * alone. */
+ * alone.  Where q_start does not ascend and sequences share tokens, attention
+ * may do nothing and set TQ1_ERR_BAD_ID. */
 typedef struct tq1_kv_batch {
   const int32_t* page_table; /* [n_seqs][max_pages] */
   const int32_t* q_start;    /* [n_seqs + 1], ascending */

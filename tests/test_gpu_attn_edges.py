@@ -116,3 +116,30 @@ def test_a_workspace_for_the_largest_batch_serves_smaller_ones(d, n_q, n_kv):
         assert L.tq1_sync_status() == 0
         want, tol = attention(b, q, 0.125, True, 0)
         assert ((out.cpu().double() - want).abs() <= rounded(tol, want, F16)).all()
+
+
+@pytest.mark.parametrize("t,n_q", [(40, 2), (300, 2), (300, 12)])
+def test_starts_that_do_not_ascend_are_refused_whole(t, n_q):
+    # Sequences that count the same tokens several times over: nothing is done.
+    L = lib()
+    b = Batch([t, 0, 0, 0, 0], [t + 20, 30, 30, 30, 30], 16, 1, 64, F16).to_gpu(L)
+    _, gq = queries(b, n_q)
+    b.gq.copy_(torch.tensor([0, t, 0, t, 0, t], dtype=torch.int32))
+    out = attend(b, gq, n_q, 0.125)
+    assert L.tq1_sync_status() == -8
+    assert (out == 7).all()
+    b.gq.copy_(b.q_start)
+    assert (attend(b, gq, n_q, 0.125) != 7).any(-1).all() and L.tq1_sync_status() == 0
+
+
+def test_starts_that_hold_anything():
+    L = lib()
+    g = torch.Generator().manual_seed(3)
+    for n_seqs, t in ((3, 20), (700, 100), (5, 700)):
+        b = Batch([t] + [0] * (n_seqs - 1), [t + 9] + [5] * (n_seqs - 1), 16, 1, 64, F16).to_gpu(L)
+        _, gq = queries(b, 4)
+        for _ in range(8):
+            b.gq.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, (n_seqs + 1,), generator=g, dtype=torch.int64).to(torch.int32))
+            b.glen.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, (n_seqs,), generator=g, dtype=torch.int64).to(torch.int32))
+            attend(b, gq, 4, 0.125)
+            assert L.tq1_sync_status() in (0, -8)
