@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   auto pages_of = [&](const WarpTile& t, int i0) {
     const int k = t.key0 + (i0 + lane) * kABlock;
     if (i0 + lane >= t.todo || k >= t.hi || k + kWarpKeys <= t.lo) return -1;
-    const int id = __ldg(b.table + static_cast<int64_t>(t.seq) * b.max_pages + (k >> c.page_shift));
+    const int id = b.table[static_cast<int64_t>(t.seq) * b.max_pages + (k >> c.page_shift)];
     if (id >= 0 && id < c.n_pages) return id;
     raise_status(status, kStatusBadId);
     return -1;
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
       const uint16_t* src = a.q + (t.sq.q0 + tok) * a.ldq + static_cast<int64_t>(qh) * D + 2 * qd;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks)) : 0u;
-        qf[ks][2 + h] = there ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 8)) : 0u;
+        qf[ks][h] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks) : 0u;
+        qf[ks][2 + h] = there ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 8) : 0u;
       }
       const int pos = t.sq.len - t.sq.n + tok;
       hi[h] = there ? (plan.causal ? min(t.sq.len, pos + 1) : t.sq.len) : 0;

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       auto page_of = [&](int key0) {
         const int key = key0 + box * k.box_keys;
         if (box >= boxes || key >= g.len || key + k.box_keys <= g.lo) return -2;
-        const int id = __ldg(k.b.table + static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift));
+        const int id = k.b.table[static_cast<int64_t>(g.seq) * k.b.max_pages + (key >> k.c.page_shift)];
         if (id >= 0 && id < k.c.n_pages) return id;
         raise_status(k.status, kStatusBadId);
         return -1;

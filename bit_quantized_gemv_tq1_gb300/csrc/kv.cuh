@@ -42,14 +42,17 @@ __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
 // --------------------------------------------------------- the sequences --
 // New tokens [q0, q0 + n) and cache length of one sequence.  The arrays are
 // device data the host has not seen, so they are clamped to what exists: no
-// index formed from them leaves the call's tensors.
+// index formed from them leaves the call's tensors.  The kernels here begin
+// while the one before them may still write what they read after their wait,
+// so none of it goes through read-only loads (__ldg), which take data that
+// does not change while a kernel runs and may be moved ahead of the wait.
 struct Seq {
   int q0, n, len;
 };
 __device__ __forceinline__ Seq load_seq(const KvBatch& b, int s) {
   Seq r;
-  int q0 = __ldg(b.q_start + s), q1 = __ldg(b.q_start + s + 1);
-  r.len = min(max(__ldg(b.kv_len + s), 0), b.max_len);
+  int q0 = b.q_start[s], q1 = b.q_start[s + 1];
+  r.len = min(max(b.kv_len[s], 0), b.max_len);
   q0 = min(max(q0, 0), b.t);
   q1 = min(max(q1, q0), b.t);
   r.q0 = q0;

@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagePool
     const int64_t first = u / per_page * per_step, pool0 = first / n;
     const int i0 = static_cast<int>(first - pool0 * n);
     if (per_step == 1) {
-      const int from = __ldg(src + i0), dest = __ldg(dst + i0);
+      const int from = src[i0], dest = dst[i0];
       if (from < 0 || from >= p.n_pages || dest < 0 || dest >= p.n_pages) {
         if (threadIdx.x == 0) raise_status(status, kStatusBadId);
         continue;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const PagePool
         to[k] = nullptr;
         if (sub >= per_step || first + sub >= pages) continue;
         const int more = (i0 + sub) / n32, i = i0 + sub - more * n32;
-        const int from = __ldg(src + i), dest = __ldg(dst + i);
+        const int from = src[i], dest = dst[i];
         if (from < 0 || from >= p.n_pages || dest < 0 || dest >= p.n_pages) {
           raise_status(status, kStatusBadId);
           continue;

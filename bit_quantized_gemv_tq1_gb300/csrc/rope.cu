@@ -29,6 +29,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kMaxRotPairs = 128;  // head_dim <= 256
 constexpr int kPer = 2;            // tokens of a CTA, where there are many
+constexpr int kRopeCtas = 6;       // CTAs an SM holds (40 registers a thread): what hides the loads
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
@@ -50,8 +51,8 @@ __device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
 // One CTA: `per` tokens from blockIdx.x * per on, and of each token's heads
 // (of q, k and v) the blockIdx.y-th part of gridDim.y.
 template <typename TI, typename TO>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache c, const KvBatch b, const RopeArgs a,
-                                                                   int per, int one_wave, unsigned* status) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+    rope_append_kernel(const KvCache c, const KvBatch b, const RopeArgs a, int per, int one_wave, unsigned* status) {
   __shared__ float2 s_cs[kPer][kMaxRotPairs];
   __shared__ int s_seq[kPer], s_pos[kPer], s_page[kPer];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -96,19 +97,30 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache
   if (one_wave) pdl_launch_dependents();
   pdl_wait();
   fetch();  // on their way while the tokens' places are looked up
+  // One angle per thread: pair ap of token at.
+  static_assert(kPer == 2 && kPer * kMaxRotPairs <= kRopeThreads, "an angle per thread");
+  const int at = tid >= pairs, ap = tid - at * pairs;
+  const bool angle = tid < per * pairs && tok0 + at < b.t;
+  const float freq = angle ? a.inv_freq[ap] : 0.0f;
   // The sequence of each token, its position and its page: a warp per token.
   if (warp < per) {
     const int tok = tok0 + warp;
     int seq = -1, pos = 0, page = -1;
     if (tok < b.t) {
       int count = 0;  // sequences that end at or before this token
-      for (int s = lane; s < b.n_seqs; s += 32) count += __ldg(b.q_start + s + 1) <= tok;
+      for (int s = lane; s < b.n_seqs; s += 32) count += b.q_start[s + 1] <= tok;
       count = __reduce_add_sync(0xffffffffu, count);
-      if (count < b.n_seqs && __ldg(b.q_start + count) <= tok) {
+      int begin = b.t, end = 0, len = 0;  // of the sequence, read at once
+      if (count < b.n_seqs) {
+        begin = b.q_start[count];
+        end = b.q_start[count + 1];
+        len = b.kv_len[count];
+      }
+      if (begin <= tok) {
         seq = count;
-        pos = __ldg(b.kv_len + seq) - (__ldg(b.q_start + seq + 1) - tok);
+        pos = len - (end - tok);
         if (pos >= 0 && pos < b.max_len) {
-          page = __ldg(b.table + static_cast<int64_t>(seq) * b.max_pages + (pos >> c.page_shift));
+          page = b.table[static_cast<int64_t>(seq) * b.max_pages + (pos >> c.page_shift)];
           if (page < 0 || page >= c.n_pages) page = -1;
         }
         if (page < 0 && lane == 0 && blockIdx.y == 0) raise_status(status, kStatusBadId);
@@ -121,15 +133,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const KvCache
     }
   }
   __syncthreads();
-  for (int i = tid; i < per * pairs; i += kRopeThreads) {
-    const int t = i / pairs, p = i - t * pairs;
-    if (s_seq[t] < 0) continue;
-    const int pos = a.positions ? __ldg(a.positions + tok0 + t) : s_pos[t];
-    double half_turns = static_cast<double>(pos) * static_cast<double>(__ldg(a.inv_freq + p)) * 0.31830988618379067154;
+  if (angle && s_seq[at] >= 0) {
+    const int pos = a.positions ? a.positions[tok0 + at] : s_pos[at];
+    double half_turns = static_cast<double>(pos) * static_cast<double>(freq) * 0.31830988618379067154;
     half_turns -= 2.0 * rint(0.5 * half_turns);
     float sn, cs;
     sincospif(static_cast<float>(half_turns), &sn, &cs);
-    s_cs[t][p] = make_float2(cs * a.mscale, sn * a.mscale);
+    s_cs[at][ap] = make_float2(cs * a.mscale, sn * a.mscale);
   }
   __syncthreads();
   for (; u >= 0; fetch()) {
