@@ -70,9 +70,9 @@ struct DqSeg {
 };
 
 template <bool F16, int FMT>
-__global__ void __launch_bounds__(kDqThreads) dequant_kernel(const uint8_t* __restrict__ blocks,
-                                                             const int32_t* __restrict__ row_ids, int64_t n_out,
-                                                             void* __restrict__ out, int64_t n, int nb,
+__global__ void __launch_bounds__(kDqThreads) dequant_kernel(const uint8_t* blocks,
+                                                             const int32_t* row_ids, int64_t n_out,
+                                                             void* out, int64_t n, int nb,
                                                              unsigned* status) {
   constexpr int kBB = fmt_block_bytes<FMT>();
   constexpr int kSlot = dq_slot_bytes<FMT>();
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kDqThreads) dequant_kernel(const uint8_t* __re
         const int64_t i = u / nb;
         const int b = static_cast<int>(u - i * nb);
         len = min(len, nb - b);
-        const int64_t srow = __ldg(row_ids + i);
+        const int64_t srow = row_ids[i];
         if (srow < 0 || srow >= n) {
           if (lane == 0 && b == 0) raise_status(status, kStatusBadId);
           ok = false;  // the output row is left untouched

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1) mmv_mma_kernel(const MmaArgs a
         const int c = c0 + 32 * h;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(src_tok + c * kQ8Bytes);
 #pragma unroll
-        for (int e = 0; e < 9; ++e) wq[h][e] = (live && c < bc * 8) ? __ldg(src + e) : 0u;
+        for (int e = 0; e < 9; ++e) wq[h][e] = (live && c < bc * 8) ? src[e] : 0u;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

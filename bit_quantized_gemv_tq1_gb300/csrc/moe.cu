@@ -21,9 +21,9 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
   return m;
 }
 
-__global__ void __launch_bounds__(kCompactThreads) moe_compact_kernel(const int32_t* __restrict__ ids, int64_t pairs,
+__global__ void __launch_bounds__(kCompactThreads) moe_compact_kernel(const int32_t* ids, int64_t pairs,
                                                                        int n_experts, int chunk, int row_blocks,
-                                                                       int32_t* __restrict__ ws, unsigned* status) {
+                                                                       int32_t* ws, unsigned* status) {
   extern __shared__ int s_cnt[];  // n_experts counters, reused as scatter cursors
   pdl_launch_dependents();
   pdl_wait();

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kMThreads, 3) moe_small_kernel(const MoeArgs a
     for (int i = tid; i < ne; i += kMThreads) t_cnt[i] = 0;
     __syncthreads();
     for (int64_t p = tid; p < a.pairs; p += kMThreads) {
-      const int e = __ldg(a.ids + p);
+      const int e = a.ids[p];
       if (e >= 0 && e < ne) atomicAdd(&t_cnt[e], 1);
       else if (blockIdx.x == 0) raise_status(a.status, kStatusBadId);
     }
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kMThreads, 3) moe_small_kernel(const MoeArgs a
     if (warp == 0) {  // stable scatter of pair indices, 32 at a time, in order
       for (int64_t base = 0; base < a.pairs; base += 32) {
         const int64_t p = base + lane;
-        int e = p < a.pairs ? __ldg(a.ids + p) : -1;
+        int e = p < a.pairs ? a.ids[p] : -1;
         if (e >= ne || e < -1) e = -1;
         const uint32_t peers = __match_any_sync(0xffffffffu, e);
         const int rank = __popc(peers & ((1u << lane) - 1u));
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kDThreads, 2) moe_direct_kernel(const DirectAr
   }
   __syncthreads();  // the barriers are initialised before any thread arms one
   pdl_wait();  // ids and activations may come from the previous kernel
-  const int e = __ldg(a.ids + pair);
+  const int e = a.ids[pair];
   if (e < 0 || e >= a.n_experts) {
     if (tid == 0 && rb == 0) raise_status(a.status, kStatusBadId);
     return;  // no copy was issued

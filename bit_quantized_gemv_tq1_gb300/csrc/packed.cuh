@@ -272,7 +272,7 @@ __device__ __forceinline__ void quantize_precord_half(const float* xs, uint32_t*
   float v[16];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const float4 f = live ? __ldg(reinterpret_cast<const float4*>(xs + 16 * h) + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 f = live ? reinterpret_cast<const float4*>(xs + 16 * h)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
     v[4 * q] = f.x;
     v[4 * q + 1] = f.y;
     v[4 * q + 2] = f.z;
@@ -316,11 +316,11 @@ __device__ __forceinline__ void quantize_precord_half(const float* xs, uint32_t*
 // Build one chunk (j) of one column's record from its Q8_1 block (global).
 __device__ __forceinline__ void fill_precord_chunk(const uint8_t* blk, uint32_t* rec, int j) {
   const uint32_t* s = reinterpret_cast<const uint32_t*>(blk);
-  const uint32_t ds = __ldg(s);
+  const uint32_t ds = s[0];
   int sum = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    const uint32_t q = __ldg(s + 1 + w);
+    const uint32_t q = s[1 + w];
     rec[8 * w + j] = q;
     sum = __dp4a(static_cast<int>(q), 0x01010101, sum);
   }

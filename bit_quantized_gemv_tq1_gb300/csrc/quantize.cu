@@ -30,8 +30,8 @@ __device__ __forceinline__ int warp_sum(int v) {
 // One warp per 256-weight block.  Lane i (< 32) packs qs[i] from elements
 // i + 32c (c < 5); lanes 0..15 also pack qs[32 + i] from 160 + i + 16c;
 // lanes 16..19 pack qh[i - 16] from 240 + (i - 16) + 4c (c < 4).
-__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_kernel(const float* __restrict__ w,
-                                                                          uint8_t* __restrict__ out,
+__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_kernel(const float* w,
+                                                                          uint8_t* out,
                                                                           int64_t nblocks) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_kernel(const 
 // c % 4 of bytes 32(c/4) .. 32(c/4)+31): one warp per 256-weight block, lane
 // i packs qs[i] from elements i + 32f and qs[32 + i] from 128 + i + 32f
 // (f < 4).  Same scale and rounding as the TQ1_0 encoder.
-__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_tq2_kernel(const float* __restrict__ w,
-                                                                              uint8_t* __restrict__ out,
+__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_tq2_kernel(const float* w,
+                                                                              uint8_t* out,
                                                                               int64_t nblocks) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_rows_tq2_kernel(co
 // admitted while those waves are still being placed ends up unevenly spread
 // over the SMs (measured: a following chain of one-CTA-per-SM mat-vec
 // launches ran ~50% slower).  Dependents start as its CTAs retire.
-__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_acts_kernel(const float* __restrict__ x,
-                                                                          uint8_t* __restrict__ out,
+__global__ void __launch_bounds__(kWarpsPerCta * 32) quantize_acts_kernel(const float* x,
+                                                                          uint8_t* out,
                                                                           int64_t nblocks) {
   pdl_wait();
   const int lane = threadIdx.x & 31;

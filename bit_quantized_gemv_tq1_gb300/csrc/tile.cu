@@ -319,9 +319,9 @@ __global__ void __launch_bounds__(kPrepThreads) tile_prep_kernel(const uint8_t* 
   uint32_t gq[kPrepHeld][2], gd[kPrepHeld];
   auto load_group = [&](int i, uint32_t& q0, uint32_t& q1, uint32_t& d) {
     const uint32_t* b = reinterpret_cast<const uint32_t*>(qr + (i >> 2) * kQ8Bytes);
-    d = __ldg(b) & 0xFFFFu;
-    q0 = __ldg(b + 1 + 2 * (i & 3));
-    q1 = __ldg(b + 2 + 2 * (i & 3));
+    d = b[0] & 0xFFFFu;
+    q0 = b[1 + 2 * (i & 3)];
+    q1 = b[2 + 2 * (i & 3)];
   };
   float m = 0.0f;
   if (held) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kPrepThreads) tile_prep_kernel(const uint8_t* 
     }
   } else {
     for (int j = tid; j < nq; j += kPrepThreads)
-      m = fmaxf(m, fabsf(__half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(qr + j * kQ8Bytes))))));
+      m = fmaxf(m, fabsf(__half2float(__ushort_as_half(*reinterpret_cast<const unsigned short*>(qr + j * kQ8Bytes)))));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const uint32_t aph = static_cast<uint32_t>(u) & 1u;
       // Scales of this tile's tokens, fetched while the MMAs run.
       __syncwarp();
-      for (int tl = c_lo + lane; tl < c_lo + TOK / 2; tl += 32) tsc[tl] = __ldg(a.scale + tok0 + tl);
+      for (int tl = c_lo + lane; tl < c_lo + TOK / 2; tl += 32) tsc[tl] = a.scale[tok0 + tl];
       __syncwarp();
       if (!warp_wait(&accf_bar, aph, abort_flag)) break;
       tc_fence_after();

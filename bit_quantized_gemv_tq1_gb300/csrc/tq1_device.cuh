@@ -351,11 +351,11 @@ __device__ __forceinline__ float block_dot(const Digits& D, const uint32_t* rec)
 // handles; eight threads fill one record.
 __device__ __forceinline__ void fill_record_chunk(const uint8_t* src, uint32_t* rec, int lane8) {
   const uint32_t* s = reinterpret_cast<const uint32_t*>(src + lane8 * kQ8Bytes);
-  const uint32_t ds = __ldg(s);
+  const uint32_t ds = s[0];
   int sum = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    const uint32_t q = __ldg(s + 1 + w);
+    const uint32_t q = s[1 + w];
     rec[8 * lane8 + w] = q;
     sum = __dp4a(static_cast<int>(q), 0x01010101, sum);
   }
