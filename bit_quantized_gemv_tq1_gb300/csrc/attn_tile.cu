@@ -828,6 +828,8 @@ int attn_tile_rows(int group, bool pair) { return (kTRows / group) * group * (pa
 int launch_attn_tile(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool pair, int ctas, Part* parts,
                      float* slots, unsigned* status, cudaStream_t s) {
   const int group = a.n_q / c.n_kv, tokens = kTRows / group;
+  // Heads or pages that are all the same one: not a tensor map's strides.
+  if ((c.n_kv > 1 && c.head_stride == 0) || (c.n_pages > 1 && c.page_stride == 0)) return TQ1_ERR_UNSUPPORTED;
   TileKernelArgs k = {};
   k.c = c;
   k.b = b;

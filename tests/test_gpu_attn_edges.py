@@ -143,3 +143,20 @@ def test_starts_that_hold_anything():
             b.glen.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, (n_seqs,), generator=g, dtype=torch.int64).to(torch.int32))
             attend(b, gq, 4, 0.125)
             assert L.tq1_sync_status() in (0, -8)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [30], [200, 3]])
+def test_heads_that_share_their_pages(new):
+    # Head stride 0: all kv heads read the same keys and values.
+    L = lib()
+    b = Batch(new, [n + 150 for n in new], 16, 3, 128, BF16)
+    b.kv[:] = b.kv[:, :, :1].clone()
+    b.to_gpu(L)
+    one = b.gkv[:, :, :1].contiguous().expand(-1, -1, 3, -1, -1)
+    b.cache = L.tq1_kv_cache(one[0], one[1])
+    assert b.cache.head_stride == 0
+    q, gq = queries(b, 12)
+    out = attend(b, gq, 12, 0.1)
+    assert L.tq1_sync_status() == 0
+    want, tol = attention(b, q, 0.1, True, 0)
+    assert ((out.cpu().double() - want).abs() <= rounded(tol, want, BF16)).all()
