@@ -19,9 +19,10 @@
 // the tensor pipe and 400 between the roles, against 2048 of tensor work for
 // both streams.  S and P of a second block per stream would break the chain;
 // the two O leave no tensor memory for them.
-// 4096 tokens on 12288 keys, 40/8 heads of 128: 550 us, 1.56 PFLOP/s, and
-// 586 call after call, at the power limit's lower clock.  A ragged batch (1 to 1463 tokens, 24/8 heads of 64,
-// window 1024): 45.3 us, of which 5 pass before the first scores.
+// 4096 tokens on 12288 keys, 40/8 heads of 128: 580 us call after call, at the
+// power limit's lower clock, 1.48 PFLOP/s; 550 us in a short run.  A ragged
+// batch (1 to 1463 tokens, 24/8 heads of 64, window 1024): 45.9 us in a graph,
+// 47.7 a call, of which 5 pass before the first scores.
 //   PAIR:  a tile has two times 128 rows, a stream each, and both read the
 //          same keys (a chunk with more than 128 rows per kv head)
 //   else:  a tile has 128 rows; the streams take every other block and are

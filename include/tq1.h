@@ -469,8 +469,10 @@ typedef struct tq1_page_pool {
  * factor == 1 gives theta_i.  For contexts `factor` times longer than the
  * orig_len positions a model was trained on, g ramps from 0 (stretched by the
  * factor) to 1 (kept) as the turns orig_len theta_i / 2 pi of a pair go from
- * `low` to `high`; low = high = INFINITY stretches all pairs alike.  fp64,
- * rounded once.  inv_freq: fp32 [rot_dim / 2], device; rot_dim even, <= 256.
+ * `low` to `high`; low = high = INFINITY stretches all pairs alike.  (The ramp
+ * is linear in the turns.  A model whose ramp is linear in the pair's index
+ * between two indexes wants other numbers: fill inv_freq with them instead;
+ * tq1_rope_append takes any table.)  fp64, rounded once.  inv_freq: fp32 [rot_dim / 2], device; rot_dim even, <= 256.
  * No passage: a convention of this library.
  */
 int tq1_rope_freqs(float* inv_freq, int64_t rot_dim, double base, double factor, double orig_len, double low,
@@ -513,7 +515,10 @@ size_t tq1_paged_attn_workspace_size(const tq1_kv_cache* cache, int64_t t, int64
  * with K, V of kv head h / (n_q / n_kv).  Visible to the token at position p
  * are the slots j < kv_len with j <= p (causal != 0) and j > p - window
  * (window > 0).  A row that sees nothing is 0.  One call serves decode steps
- * (one token per sequence), prompt chunks and any mix of them.
+ * (one token per sequence), prompt chunks and any mix of them.  (The kernel is
+ * chosen by the average sequence's rows, t * n_q / n_kv / n_seqs: a long chunk
+ * runs faster in a call of its own than with hundreds of steps, and in a batch
+ * without the sequences that have no new tokens.)
  *   q: [t][n_q][head_dim] of the cache's type, tokens ldq elements apart
  *   out: [t][n_q][head_dim] of the cache's type, or fp32 when out_f32 != 0
  *      (what q8_1_quantize_acts takes), tokens ldo elements apart; rows of
