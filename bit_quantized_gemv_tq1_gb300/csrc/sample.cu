@@ -1343,8 +1343,10 @@ __global__ void __launch_bounds__(N, 1024 / N) sample_kernel(const SampleArgs a,
   for (;;) {
     if (tid == 0) sh.state.act = decide();
     __syncthreads();
+    // Read here: behind the next barrier thread 0 may be deciding anew.
     const int act = sh.state.act;
-    if (sh.state.leave) dismiss(ranks);
+    const bool leave = sh.state.leave, last = sh.state.last;
+    if (leave) dismiss(ranks);
     if (act == kPass) {
       if (tid < ranks) (ranks > 1 ? shared_of(tid) : sh).cmd = sh.next;
       sync_row(ranks);
@@ -1373,7 +1375,7 @@ __global__ void __launch_bounds__(N, 1024 / N) sample_kernel(const SampleArgs a,
         }
       }
       __syncthreads();
-      if (s.last) break;
+      if (last) break;
     }
   }
   if (tid == 0) {
