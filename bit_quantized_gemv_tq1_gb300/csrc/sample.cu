@@ -364,10 +364,11 @@ struct Row {
     top = r.top;
   }
 
+  // NaN is never taken; -0 equals 0.
+  __device__ __forceinline__ static float ordered(float l) { return l == l ? l + 0.0f : -INFINITY; }
+  // Of a logit of the row, once: where there are +inf, a second time would find none.
   __device__ __forceinline__ float value(float l) const {
-    l = l == l ? l + 0.0f : -INFINITY;  // NaN is never taken; -0 equals 0
-    if (top) l = l == INFINITY ? 0.0f : -INFINITY;
-    return l;
+    return top ? (l == INFINITY ? 0.0f : -INFINITY) : ordered(l);
   }
 
   // The logits of a group, as they are.
@@ -441,8 +442,8 @@ struct Row {
     } while (j < f1);
   }
 
-  // f(four logits) for this CTA's part of the row, as they are (but where there
-  // are +inf); -inf where a thread has none.  Two groups are on their way while
+  // f(four logits) for this CTA's part of the row, as they are, but where there
+  // are +inf their values; -inf where a thread has none.  Two groups are on their way while
   // two are worked on.
   template <typename F>
   __device__ __forceinline__ void each(F&& f) const {
@@ -534,7 +535,7 @@ __device__ __noinline__ void pass() {
       }
       if (flags & kByKey) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = key_of(row.value(l[i]));
+        for (int i = 0; i < 4; ++i) x[i] = key_of(Row<T, N>::ordered(l[i]));
       }
       if (!(flags & kMasses)) {
         const u64 least = sh.cmd.threshold;
