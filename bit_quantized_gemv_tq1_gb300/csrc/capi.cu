@@ -122,7 +122,7 @@ const char* tq1_status_string(int status) {
     case TQ1_ERR_WORKSPACE: return "workspace too small";
     case TQ1_ERR_CUDA: return "CUDA runtime error";
     case TQ1_ERR_TIMEOUT: return "a kernel timed out waiting for a transfer";
-    case TQ1_ERR_BAD_ID: return "routing, page or sequence id out of range";
+    case TQ1_ERR_BAD_ID: return "routing, page, sequence or token id out of range";
     case TQ1_ERR_NO_PAGES: return "no free pages, or no room in a page-table row";
     default: return "unknown status";
   }

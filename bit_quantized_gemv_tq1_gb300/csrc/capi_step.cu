@@ -108,9 +108,10 @@ int tq1_sample(const void* logits, int dtype, int64_t ld, int64_t t, int64_t v, 
   if ((reinterpret_cast<uintptr_t>(logits) & (dtype == TQ1_F32 ? 3u : 1u)) != 0 || off4(temperature) || off4(top_k) ||
       off4(top_p) || off4(min_p) || off4(u) || off4(ids) || off4(probs))
     return TQ1_ERR_ALIGN;
-  if (!status_word()) return TQ1_ERR_CUDA;
+  unsigned* st = status_word();
+  if (!st) return TQ1_ERR_CUDA;
   const SampleArgs a = {logits, ld, temperature, top_k, top_p, min_p, u, ids, probs, dtype, static_cast<int>(v)};
-  return launch_sample(a, t, static_cast<cudaStream_t>(stream));
+  return launch_sample(a, t, st, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -103,7 +103,7 @@ struct Result {
   u64 mass;    // sum of the pass
   unsigned n;  // tokens gathered
   uint32_t kmin, kmax;
-  int found;   // kFind: the token; kGather: how many of n are of the second bin alone (and kmin their smallest key)
+  int found;   // kFind: the token, plus one; kGather: how many of n are of the second bin alone (and kmin their smallest key)
   unsigned tally[kMaxCluster];
 };
 
@@ -170,7 +170,7 @@ struct State {
   u64 start, nth, one;
   // The answer.
   u64 mass_at, weight_at;
-  int token;
+  int token;          // -1: not found, which only logits that change under the call can bring about
 };
 
 // A row's filters.
@@ -689,7 +689,7 @@ __device__ __noinline__ void pass() {
         all += sh.red_at[w];
       }
       before += __popc(b & ((1u << (tid & 31)) - 1u));
-      if (hit && before + 1 == left) lead.sum.found = at;
+      if (hit && before + 1 == left) lead.sum.found = at + 1;
       __syncthreads();
       if (all >= left) break;
       left -= all;
@@ -1025,6 +1025,7 @@ __device__ __noinline__ int decide() {
           }
         }
         s.by_mass = s.question > 0;
+        if (s.question == 2) s.token = -1;
         if (s.question == 0) s.target = static_cast<u64>(f.top_k);
         else if (s.question == 1) s.target = f.top_p > 0.0f ? max(u64{1}, part_of(s.kept, f.top_p, true)) : 1;
         else s.target = pick_of(f.u, s.kept);
@@ -1102,6 +1103,11 @@ __device__ __noinline__ int decide() {
               s.khi = min(s.khi, s.klo + ((1u << s.shift) - 1u));
               if (sh.count[s.bin[0]] <= kList) {
                 TQ1_DO(ask(kByKey | kGather, s.klo, s.khi - s.klo, 0));
+                if (sh.sum.n > kList) {  // more than were counted
+                  s.token = -1;
+                  s.leave = !s.gone;
+                  return kEnd;
+                }
                 break;
               }
               if (s.klo == s.khi) {  // more tokens than the list holds share one logit: they are counted off by index
@@ -1114,7 +1120,7 @@ __device__ __noinline__ int decide() {
                   TQ1_DO(ask(kByKey | kTally, s.klo, 0, 0));
                   for (s.b0 = 0; static_cast<int>(s.b0) < sh.row.ranks - 1 && s.nth > sh.sum.tally[s.b0]; ++s.b0) s.nth -= sh.sum.tally[s.b0];
                   TQ1_DO(ask(kByKey | kFind, s.klo, 0, 0, 0, s.b0, static_cast<int>(s.nth)));
-                  s.token = sh.sum.found;
+                  s.token = sh.sum.found - 1;
                 }
                 s.found = true;
                 break;
@@ -1146,7 +1152,7 @@ __device__ __noinline__ int decide() {
 #undef TQ1_DO
 
 template <typename T, int N>
-__global__ void __launch_bounds__(N, 1024 / N) sample_kernel(const SampleArgs a, int ranks, int one_wave) {
+__global__ void __launch_bounds__(N, 1024 / N) sample_kernel(const SampleArgs a, int ranks, int one_wave, unsigned* status) {
   constexpr int kWarps = N / 32, kUnused = sizeof(T) == 2 ? (std::is_same<T, __half>::value ? 13 : 16) : 0;
   Shared& sh = shared();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1381,7 +1387,8 @@ __global__ void __launch_bounds__(N, 1024 / N) sample_kernel(const SampleArgs a,
   }
   if (tid == 0) {
     a.ids[r] = sh.state.token;
-    if (a.probs) a.probs[r] = ratio_of(sh.state.weight_at, sh.state.kept);
+    if (a.probs) a.probs[r] = sh.state.token < 0 ? 0.0f : ratio_of(sh.state.weight_at, sh.state.kept);
+    if (sh.state.token < 0) raise_status(status, kStatusBadId);
   }
 }
 
@@ -1440,9 +1447,9 @@ int64_t clusters(int dev, int ranks, bool two) {
 }
 
 template <typename T, int N>
-int launch(const SampleArgs& a, int64_t t, int ranks, int one_wave, cudaStream_t s) {
+int launch(const SampleArgs& a, int64_t t, int ranks, int one_wave, unsigned* status, cudaStream_t s) {
   Launch<T, N> l(t * ranks, ranks, sizeof(Shared), s);
-  return cuda_ok(cudaLaunchKernelEx(&l.cfg, sample_kernel<T, N>, a, ranks, one_wave)) ? TQ1_OK : TQ1_ERR_CUDA;
+  return cuda_ok(cudaLaunchKernelEx(&l.cfg, sample_kernel<T, N>, a, ranks, one_wave, status)) ? TQ1_OK : TQ1_ERR_CUDA;
 }
 
 // Rows beyond two an SM: a CTA of 256 threads each (512 rows of 32000 take 0.82
@@ -1455,12 +1462,12 @@ int launch(const SampleArgs& a, int64_t t, int ranks, int one_wave, cudaStream_t
 constexpr int kLongRow = 98304;
 
 template <typename T>
-int launch_type(const SampleArgs& a, int64_t t, cudaStream_t s) {
+int launch_type(const SampleArgs& a, int64_t t, unsigned* status, cudaStream_t s) {
   const int dev = device_info().device;
   if (dev < 0 || dev >= 64) return TQ1_ERR_CUDA;
   if (configure<T, 512>(dev) != TQ1_OK || configure<T, 256>(dev) != TQ1_OK) return TQ1_ERR_CUDA;
   const int64_t sms = std::max(1, device_info().num_sms);
-  if (t > 2 * sms) return launch<T, 256>(a, t, 1, t <= 4 * sms, s);
+  if (t > 2 * sms) return launch<T, 256>(a, t, 1, t <= 4 * sms, status, s);
   auto most = [&](bool two) {
     int ranks = kMaxCluster;
     while (ranks > 1 && (a.v < ranks * 2048 || clusters<T>(dev, ranks, two) < t)) --ranks;
@@ -1468,16 +1475,16 @@ int launch_type(const SampleArgs& a, int64_t t, cudaStream_t s) {
   };
   int ranks = most(false);
   if (ranks <= 2 && a.v >= kLongRow) ranks = most(true);
-  return launch<T, 512>(a, t, ranks, 1, s);
+  return launch<T, 512>(a, t, ranks, 1, status, s);
 }
 
 }  // namespace
 
-int launch_sample(const SampleArgs& a, int64_t t, cudaStream_t s) {
+int launch_sample(const SampleArgs& a, int64_t t, unsigned* status, cudaStream_t s) {
   switch (a.type) {
-    case kF16: return launch_type<__half>(a, t, s);
-    case kBf16: return launch_type<__nv_bfloat16>(a, t, s);
-    default: return launch_type<float>(a, t, s);
+    case kF16: return launch_type<__half>(a, t, status, s);
+    case kBf16: return launch_type<__nv_bfloat16>(a, t, status, s);
+    default: return launch_type<float>(a, t, status, s);
   }
 }
 

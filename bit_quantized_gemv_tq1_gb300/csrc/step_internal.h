@@ -50,6 +50,6 @@ struct SampleArgs {
   float* probs;  // [t], or nullptr
   int type, v;
 };
-int launch_sample(const SampleArgs& a, int64_t t, cudaStream_t s);
+int launch_sample(const SampleArgs& a, int64_t t, unsigned* status, cudaStream_t s);
 
 }  // namespace tq1

@@ -70,7 +70,7 @@ enum tq1_status {
   TQ1_ERR_WORKSPACE = -5,   /* workspace too small */
   TQ1_ERR_CUDA = -6,        /* a CUDA runtime call failed */
   TQ1_ERR_TIMEOUT = -7,     /* a kernel gave up waiting on a transfer (device status) */
-  TQ1_ERR_BAD_ID = -8,      /* a routing, page or sequence id was out of range (device status) */
+  TQ1_ERR_BAD_ID = -8,      /* a routing, page, sequence or token id was out of range (device status) */
   TQ1_ERR_NO_PAGES = -9     /* no free pages, or no room in a page-table row (device status) */
 };
 
@@ -671,7 +671,9 @@ int tq2_moe(const void* gate, const void* up, const void* down, int64_t n_expert
  * temperature that is not above 2^-100 takes the first token of the order, with
  * probability 1; u below 0 counts as 0, from 1 on (or NaN) as just below 1.
  * Logits that are NaN or -inf are never taken (a row of nothing else: id -1,
- * probability 0); where there are +inf, they alone are.
+ * probability 0); where there are +inf, they alone are.  Logits must not change
+ * under the call: a row that finds no token because they did gets id -1 and
+ * probability 0 and sets TQ1_ERR_BAD_ID.
  * Weights are held as integers in units of 2^-44 and added exactly: the same
  * tokens whatever the batch.  v <= 2^19, t <= 2^20.  No workspace.
  * No passage: a convention of this library.
