@@ -67,6 +67,20 @@ struct RowOf {
 };
 
 template <typename TD>
+__device__ __forceinline__ RowOf row_of(const NormArgs& a, int64_t row) {
+  const int64_t at = row * a.k;
+  RowOf r;
+  r.x = a.x + at;
+  if constexpr (!std::is_same<TD, NoDelta>::value) r.delta = static_cast<const TD*>(a.delta) + at;
+  r.gamma = a.gamma;
+  r.x_out = a.x_out ? a.x_out + at : nullptr;
+  r.q8 = a.q8 ? a.q8 + row * (a.k >> 5) * 9 : nullptr;
+  r.y = a.y ? static_cast<uint8_t*>(a.y) + at * (a.y_type == kF32 ? 4 : 2) : nullptr;
+  r.y_type = a.y_type;
+  return r;
+}
+
+template <typename TD>
 __device__ __forceinline__ Eight load_x(const RowOf& r, int i) {
   Eight v = load8(r.x, i);
   if constexpr (!std::is_same<TD, NoDelta>::value) {
@@ -169,16 +183,71 @@ __device__ __forceinline__ void finish(const RowOf& r, int i, bool live, Eight v
   }
 }
 
-// 1 / sqrt(mean + eps); a row of zeros stays one.
-__device__ __forceinline__ float inverse_norm(float sum, const NormArgs& a) {
-  const float mean = __fadd_rn(__fdiv_rn(sum, static_cast<float>(a.k)), a.eps);
+__device__ __forceinline__ float mean_of(float sum, int k, float eps) { return __fadd_rn(__fdiv_rn(sum, static_cast<float>(k)), eps); }
+// 1 / sqrt(mean); a row of zeros stays one.
+__device__ __forceinline__ float inverse_root(float mean) {
   return mean > 0.0f ? __frcp_rn(__fsqrt_rn(mean)) : (mean == 0.0f ? 0.0f : mean);
+}
+
+// What a row is multiplied by, and its sum formed anew, where the squares of
+// its values leave fp32's range.  Up: below 2^-100 of a mean, what squares
+// below 2^-126 lose (2^-150 each) would no longer be lost beside it; values, at most
+// 2^-50 sqrt(k), then lie in 2^-49 .. 2^60.  Down: values lie below 2^53, their
+// squares' sum below 2^126; those that lose bits are below 2^-126 in y.
+__device__ __forceinline__ float factor_of(float mean) {
+  if (mean >= 7.888609052210118e-31f && mean < INFINITY) return 1.0f;
+  return mean < 1.0f ? 1.2676506002282294e30f : 2.6469779601696886e-23f;  // 2^100, 2^-75
+}
+__device__ __forceinline__ Eight times(const Eight& v, float by) {
+  return {make_float4(v.a.x * by, v.a.y * by, v.a.z * by, v.a.w * by), make_float4(v.b.x * by, v.b.y * by, v.b.z * by, v.b.w * by)};
+}
+
+// The sum over a block, by all threads, through `part`, which the threads may
+// read until the block's next barrier.
+__device__ __forceinline__ float block_sum(float sum, float* part) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) part[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = lane < (blockDim.x >> 5) ? part[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// A row once more, by all threads, if its squares leave fp32's range: read from
+// where it is (x' where that has been stored).  Not inlined, and for rows copied
+// ahead behind the others: such a branch among them costs all rows (4096 of 5120
+// with a bf16 delta 43.5 us, with the branch in the loop 44.5).
+template <typename TD>
+__device__ __noinline__ void far_row(const RowOf r, int k, float eps, float* part) {
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x, groups = k >> 3;
+  auto load = [&](int i) { return r.x_out ? load8(r.x_out, i) : load_x<TD>(r, i); };
+  float by = 1.0f, mean;
+  for (;;) {
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int i = tid; i < groups; i += threads) sum = square_sum(times(load(i), by), sum);
+    __syncthreads();  // part may still be read
+    mean = mean_of(block_sum(sum, part), k, eps * by * by);
+    if (by != 1.0f) break;
+    by = factor_of(mean);
+    if (by == 1.0f) return;
+  }
+  const float inv = inverse_root(mean);
+#pragma unroll 1
+  for (int i = tid; i - lane < groups; i += threads) {
+    Eight w = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (i < groups) w = times(load(i), by);
+    finish(r, i, i < groups, w, inv);
+  }
 }
 
 template <typename TD, int NV>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int one_wave) {
   __shared__ float s_part[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
   const int groups = a.k >> 3;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * a.k;
   RowOf r;
@@ -201,7 +270,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int on
       if (i < groups) v[j] = load_x<TD>(r, i);
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j) sum = square_sum(v[j], sum);
+    for (int j = 0; j < NV; ++j) {
+      if (r.x_out && tid + j * threads < groups) store_x(r, tid + j * threads, v[j]);
+      sum = square_sum(v[j], sum);
+    }
   } else {
     for (int i = tid; i < groups; i += threads) {
       const Eight w = load_x<TD>(r, i);
@@ -209,19 +281,29 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int on
       sum = square_sum(w, sum);
     }
   }
+  sum = block_sum(sum, s_part);
+  float mean = mean_of(sum, a.k, a.eps);
+  const float by = factor_of(mean);
+  if (by != 1.0f) {  // of all threads
+    sum = 0.0f;
+    if constexpr (NV > 0) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_part[warp] = sum;
-  __syncthreads();
-  sum = lane < (threads >> 5) ? s_part[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = inverse_norm(sum, a);
+      for (int j = 0; j < NV; ++j) {
+        v[j] = times(v[j], by);
+        sum = square_sum(v[j], sum);
+      }
+    } else {
+      far_row<TD>(r, a.k, a.eps, s_part);
+      return;
+    }
+    __syncthreads();
+    mean = mean_of(block_sum(sum, s_part), a.k, a.eps * by * by);
+  }
+  const float inv = inverse_root(mean);
   if constexpr (NV > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * threads;
-      if (r.x_out && i < groups) store_x(r, i, v[j]);
       finish(r, i, i < groups, v[j], inv);
     }
   } else {
@@ -263,15 +345,10 @@ __global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a, i
       if (blockIdx.x + static_cast<int64_t>(i) * gridDim.x < t) fetch(blockIdx.x + static_cast<int64_t>(i) * gridDim.x, i);
   int slot = 0;
   uint32_t phase = 0;
+  bool far = false;  // whether a row is left for the end; the same for all threads
 #pragma unroll 1
   for (int64_t row = blockIdx.x, turn = 0; row < t; row += gridDim.x, ++turn) {
-    const int64_t at = row * a.k;
-    RowOf r;
-    r.gamma = a.gamma;
-    r.x_out = a.x_out ? a.x_out + at : nullptr;
-    r.q8 = a.q8 ? a.q8 + row * (a.k >> 5) * 9 : nullptr;
-    r.y = a.y ? static_cast<uint8_t*>(a.y) + at * (a.y_type == kF32 ? 4 : 2) : nullptr;
-    r.y_type = a.y_type;
+    RowOf r = row_of<TD>(a, row);
     r.x = reinterpret_cast<const float*>(smem + slot * (x_bytes + d_bytes));
     r.delta = smem + slot * (x_bytes + d_bytes) + x_bytes;
     const bool ok = mbar_wait(&bars[slot], phase);
@@ -302,7 +379,9 @@ __global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a, i
     sum = lane < (threads >> 5) ? s_part[turn & 1][lane] : 0.0f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = inverse_norm(sum, a);
+    const float mean = mean_of(sum, a.k, a.eps);
+    far |= factor_of(mean) != 1.0f;
+    const float inv = inverse_root(mean);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = tid + j * threads;
@@ -310,6 +389,8 @@ __global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a, i
       finish(r, i, i < groups, v[j], inv);
     }
   }
+  if (far)
+    for (int64_t row = blockIdx.x; row < t; row += gridDim.x) far_row<TD>(row_of<TD>(a, row), a.k, a.eps, s_part[0]);
 }
 
 template <typename TD, int NV>

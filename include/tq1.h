@@ -607,10 +607,10 @@ int tq1_pages_compact(const tq1_page_pool* pool, void* ws, size_t ws_bytes, void
  *   x_out: fp32 [t][k], or NULL; it may be x (in place), else no overlap
  *   q8: [t][k/32] Q8_1 blocks, y: [t][k] of type y_dtype; one of them may be NULL
  * k is a positive multiple of 32, at most 2^20; t <= 2^24; eps >= 0.  Sums are
- * fp32 (|x'| < 10^18; a row that holds values that are not finite gets any
- * values, the others theirs).  q8 equals q8_1_quantize_acts of the y that
- * y_dtype == TQ1_F32 gives, bit for bit.  A row of zeros stays zero, with
- * eps == 0 too.  Deterministic.
+ * fp32, of the row times a power of two where its own squares leave that range
+ * (a row that holds values that are not finite gets any values, the others
+ * theirs).  q8 equals q8_1_quantize_acts of the y that y_dtype == TQ1_F32 gives,
+ * bit for bit.  A row of zeros stays zero, with eps == 0 too.  Deterministic.
  * No passage: a convention of this library.
  */
 int tq1_rms_norm(const float* x, const void* delta, int delta_dtype, const float* gamma, float eps, float* x_out, void* q8,
