@@ -951,13 +951,19 @@ bool shares(const MoeLayerArgs& a, int fmt) {
   return (pairs - chunks) * 3.0 * a.k * a.f > (fmt == kFmtTq2 ? 3e8 : 2e8);
 }
 
+// Where the rows are too long for the one, the other may have room: the shared
+// form stages 8 of them at a time, but keeps tables.
+template <int FMT>
+int launch_format(const MoeLayerArgs& a, uint8_t* ws, unsigned* status, cudaStream_t s) {
+  const bool shared = shares(a, FMT);
+  const int rc = shared ? launch_tasks<FMT>(a, ws, status, s) : launch_pairs<FMT>(a, ws, status, s);
+  if (rc != TQ1_ERR_UNSUPPORTED) return rc;  // else nothing was launched
+  return shared ? launch_pairs<FMT>(a, ws, status, s) : launch_tasks<FMT>(a, ws, status, s);
+}
+
 int launch_moe_layer(const MoeLayerArgs& a, int fmt, void* ws, unsigned* status, cudaStream_t s) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  if (shares(a, fmt)) {
-    const int rc = fmt == kFmtTq2 ? launch_tasks<kFmtTq2>(a, w, status, s) : launch_tasks<kFmtTq1>(a, w, status, s);
-    if (rc != TQ1_ERR_UNSUPPORTED) return rc;  // else: a task's tables leave no room for such long rows; nothing was launched
-  }
-  return fmt == kFmtTq2 ? launch_pairs<kFmtTq2>(a, w, status, s) : launch_pairs<kFmtTq1>(a, w, status, s);
+  return fmt == kFmtTq2 ? launch_format<kFmtTq2>(a, w, status, s) : launch_format<kFmtTq1>(a, w, status, s);
 }
 
 }  // namespace tq1
