@@ -31,7 +31,7 @@ int moe(const void* gate, const void* up, const void* down, int64_t n_experts, c
       !std::isfinite(scale))
     return TQ1_ERR_SHAPE;
   if (!is_type(out_dtype) || k > kMaxMoeK || f > kMaxMoeK || n_experts > kMaxExperts || top_k > kMaxTopK || t > kMaxPairs ||
-      t * top_k > kMaxPairs)
+      t * top_k > kMaxPairs || !moe_layer_serves(fmt, n_experts, k, f, t * top_k))
     return TQ1_ERR_UNSUPPORTED;
   if (t == 0) return TQ1_OK;
   if (!gate || !up || !down || !q8 || !logits || !out || !ws) return TQ1_ERR_NULL;
@@ -82,6 +82,7 @@ size_t tq1_moe_workspace_size(int64_t n_experts, int64_t k, int64_t f, int64_t t
   if (t < 0 || k <= 0 || f <= 0 || k % kQK != 0 || f % kQK != 0 || n_experts <= 0 || top_k <= 0 || top_k > n_experts ||
       k > kMaxMoeK || f > kMaxMoeK || n_experts > kMaxExperts || top_k > kMaxTopK || t > kMaxPairs || t * top_k > kMaxPairs)
     return 0;
+  if (!moe_layer_serves(kFmtTq1, n_experts, k, f, t * top_k) && !moe_layer_serves(kFmtTq2, n_experts, k, f, t * top_k)) return 0;
   return moe_layer_workspace_bytes(k, f, t, top_k);
 }
 

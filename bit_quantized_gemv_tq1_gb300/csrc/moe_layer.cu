@@ -839,7 +839,6 @@ int launch_pairs(const MoeLayerArgs& a, uint8_t* h8, unsigned* status, cudaStrea
   while (slots > 1 && down_layout(nbf, kBB, static_cast<int>(rows), slots).total > kMaxSmem / 2) --slots;
   while (rows > 4 && down_layout(nbf, kBB, static_cast<int>(rows), slots).total > kMaxSmem) rows -= 4;
   const DownLayout down = down_layout(nbf, kBB, static_cast<int>(rows), slots);
-  if (up.total > kMaxSmem || down.total > kMaxSmem) return TQ1_ERR_UNSUPPORTED;
   // While every SM has two CTAs at most, twice the threads: one token of eight
   // experts of 768 x 2048 11.2 -> 10.8 us (five tokens 20.2 -> 24.1, so not there).
   const int64_t ctas = static_cast<int64_t>(a.t) * a.top_k * (a.f / kHRows);
@@ -851,6 +850,25 @@ int launch_pairs(const MoeLayerArgs& a, uint8_t* h8, unsigned* status, cudaStrea
   if (rc != TQ1_OK) return rc;
   return run(moe_down_kernel<FMT>, a.t * ((a.k + rows - 1) / rows), kThreads, down.total, s, a, static_cast<const uint8_t*>(h8),
              static_cast<int>(rows), slots, status);
+}
+
+// Whether the one form and the other have room for such rows: one pair's, and
+// in the shared form four or eight rows at a time beside its table.
+template <int FMT>
+bool pairs_fit(int nb, int nbf) {
+  constexpr int kBB = fmt_block_bytes<FMT>();
+  return up_layout(nb, kBB, 1).total <= kMaxSmem && down_layout(nbf, kBB, 4, 1).total <= kMaxSmem;
+}
+template <int FMT>
+bool tasks_fit(int nb, int nbf, int n_experts, int pairs) {
+  constexpr int kBB = fmt_block_bytes<FMT>();
+  const uint32_t table = table_bytes(n_experts, pairs);
+  return up_task_layout(nb, kBB, 1, kHRows / 4).total + table <= kMaxSmem && down_task_layout(nbf, kBB, 4, 1).total + table <= kMaxSmem;
+}
+template <int FMT>
+bool serves(int n_experts, int64_t k, int64_t f, int64_t pairs) {
+  const int nb = static_cast<int>(k / kQK), nbf = static_cast<int>(f / kQK);
+  return pairs_fit<FMT>(nb, nbf) || tasks_fit<FMT>(nb, nbf, n_experts, static_cast<int>(pairs));
 }
 
 // The workspace: h, and for the task kernels ids, weights and the pairs' products.
@@ -908,7 +926,6 @@ int launch_tasks(const MoeLayerArgs& a, uint8_t* ws, unsigned* status, cudaStrea
   while (rows > 4 && down_size(rows, most_down) > kThirdSmem) rows -= 4;
   while (most_down > 1 && down_size(rows, most_down) > kHalfSmem) --most_down;
   const size_t up_bytes = up_size(most, stage_rows), down_bytes = down_size(rows, most_down);
-  if (up_bytes > kMaxSmem || down_bytes > kMaxSmem) return TQ1_ERR_UNSUPPORTED;
   if (configure(reinterpret_cast<const void*>(moe_up_tasks_kernel<FMT>), 4 * FMT + 2) != TQ1_OK ||
       configure(reinterpret_cast<const void*>(moe_down_tasks_kernel<FMT>), 4 * FMT + 3) != TQ1_OK)
     return TQ1_ERR_CUDA;
@@ -937,6 +954,11 @@ int launch_tasks(const MoeLayerArgs& a, uint8_t* ws, unsigned* status, cudaStrea
 
 }  // namespace
 
+bool moe_layer_serves(int fmt, int64_t n_experts, int64_t k, int64_t f, int64_t pairs) {
+  return fmt == kFmtTq2 ? serves<kFmtTq2>(static_cast<int>(n_experts), k, f, pairs)
+                        : serves<kFmtTq1>(static_cast<int>(n_experts), k, f, pairs);
+}
+
 size_t moe_layer_workspace_bytes(int64_t k, int64_t f, int64_t t, int64_t top_k) { return workspace(k, f, t * top_k).total; }
 
 // Whether tokens that share experts share their expansion: where that saves
@@ -951,14 +973,13 @@ bool shares(const MoeLayerArgs& a, int fmt) {
   return (pairs - chunks) * 3.0 * a.k * a.f > (fmt == kFmtTq2 ? 3e8 : 2e8);
 }
 
-// Where the rows are too long for the one, the other may have room: the shared
-// form stages 8 of them at a time, but keeps tables.
+// Where the rows are too long for the one form, the other has room (which the
+// caller has seen to): the shared one stages 8 of them at a time, but keeps a table.
 template <int FMT>
 int launch_format(const MoeLayerArgs& a, uint8_t* ws, unsigned* status, cudaStream_t s) {
-  const bool shared = shares(a, FMT);
-  const int rc = shared ? launch_tasks<FMT>(a, ws, status, s) : launch_pairs<FMT>(a, ws, status, s);
-  if (rc != TQ1_ERR_UNSUPPORTED) return rc;  // else nothing was launched
-  return shared ? launch_pairs<FMT>(a, ws, status, s) : launch_tasks<FMT>(a, ws, status, s);
+  const int nb = a.k / kQK, nbf = a.f / kQK;
+  const bool tasks = shares(a, FMT) ? tasks_fit<FMT>(nb, nbf, a.n_experts, a.t * a.top_k) : !pairs_fit<FMT>(nb, nbf);
+  return tasks ? launch_tasks<FMT>(a, ws, status, s) : launch_pairs<FMT>(a, ws, status, s);
 }
 
 int launch_moe_layer(const MoeLayerArgs& a, int fmt, void* ws, unsigned* status, cudaStream_t s) {

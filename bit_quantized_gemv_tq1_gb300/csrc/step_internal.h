@@ -36,6 +36,8 @@ struct MoeLayerArgs {
   int renormalize, out_type;
   float scale;
 };
+// Whether the kernels have room for such rows in shared memory.
+bool moe_layer_serves(int fmt, int64_t n_experts, int64_t k, int64_t f, int64_t pairs);
 size_t moe_layer_workspace_bytes(int64_t k, int64_t f, int64_t t, int64_t top_k);
 int launch_moe_layer(const MoeLayerArgs& a, int fmt, void* ws, unsigned* status, cudaStream_t s);
 

@@ -616,8 +616,9 @@ int tq1_pages_compact(const tq1_page_pool* pool, void* ws, size_t ws_bytes, void
 int tq1_rms_norm(const float* x, const void* delta, int delta_dtype, const float* gamma, float eps, float* x_out, void* q8,
                  void* y, int y_dtype, int64_t t, int64_t k, void* stream);
 
-/* Workspace bytes of tq1_moe / tq2_moe (0: arguments they refuse).  It grows
- * with t and top_k: one for the largest call serves smaller ones.
+/* Workspace bytes of tq1_moe / tq2_moe (0: arguments that both refuse; the
+ * longest rows only tq1_moe takes).  It grows with t and top_k: one for the
+ * largest call serves smaller ones.
  * No passage: a convention of this library. */
 size_t tq1_moe_workspace_size(int64_t n_experts, int64_t k, int64_t f, int64_t t, int64_t top_k);
 
@@ -641,9 +642,10 @@ size_t tq1_moe_workspace_size(int64_t n_experts, int64_t k, int64_t f, int64_t t
  * id -1 and weight 0 in the places left, one with none gets res (or 0).
  * Equal +inf logits share the weight.  One matrix for all tokens (an ordinary
  * gated layer) is n_experts = top_k = 1.
- * k, f: positive multiples of 256, k up to 10240 (longer rows where they fit the
- * kernels' shared memory, else TQ1_ERR_UNSUPPORTED and nothing is launched), f up
- * to 65536; n_experts <= 1024; top_k <= 32 and <= n_experts; t * top_k <= 4096.
+ * k, f: positive multiples of 256, k up to 16384 with f up to 49152, or k up to
+ * 10240 with f up to 65536 (longer rows where they fit the kernels' shared memory,
+ * else TQ1_ERR_UNSUPPORTED: the larger k, f, n_experts and t * top_k, and TQ2_0, need
+ * more); n_experts <= 1024; top_k <= 32 and <= n_experts; t * top_k <= 4096.
  * Deterministic.
  * No passage: a convention of this library.
  */

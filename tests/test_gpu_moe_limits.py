@@ -33,3 +33,10 @@ def test_a_token_alone_and_in_a_batch_on_long_rows(tq, fmt):
     for i in (0, 33, 69):
         layer.call(q8[i:i + 1].clone(), logits[i:i + 1].clone(), 2, one)
         assert torch.equal(one[0], many[i])
+
+
+@pytest.mark.parametrize("fmt,k,f,t,experts", [("tq2", 16384, 49152, 2, 1), ("tq1", 16384, 49152, 1, 1), ("tq1", 22528, 256, 2, 2), ("tq2", 256, 55040, 30, 1),
+                                               ("tq2", 16384, 256, 40, 1024)])
+def test_the_longest_rows_that_are_taken(tq, fmt, k, f, t, experts):
+    Layer(tq, fmt, experts, k, f, seed=5).check(t, 1)
+    torch.cuda.empty_cache()
