@@ -8,7 +8,10 @@
 // between the sum of squares and the scaling (NV = 0: rows too long for that
 // are read again), four neighbouring lanes hold a Q8_1 block: two shuffles
 // give its maximum and its sum.  Sums of squares are fp32, a thread's in order,
-// then by shuffles: the same whatever the other rows.
+// then by shuffles: the same bits in every call of as many rows.  How many groups a
+// thread has goes by the number of rows, so a row may have other last bits in a batch
+// of another size.  (The same order whatever the batch, spans of 32 groups at a time,
+// took 2 to 4% more of many rows without a delta.)
 //
 // A few rows wait for their loads, then for the row's sum: a row of 6144 takes
 // 3.2 us in a sequence of calls, 48 rows of 5120 with an fp32 delta 3.5.  Many

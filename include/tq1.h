@@ -610,7 +610,9 @@ int tq1_pages_compact(const tq1_page_pool* pool, void* ws, size_t ws_bytes, void
  * fp32, of the row times a power of two where its own squares leave that range
  * (a row that holds values that are not finite gets any values, the others
  * theirs).  q8 equals q8_1_quantize_acts of the y that y_dtype == TQ1_F32 gives,
- * bit for bit.  A row of zeros stays zero, with eps == 0 too.  Deterministic.
+ * bit for bit.  A row of zeros stays zero, with eps == 0 too.  Deterministic: the
+ * same bits in every call of the same t and k; the sum's order goes by t too, so a
+ * row may have other last bits in a batch of another size.
  * No passage: a convention of this library.
  */
 int tq1_rms_norm(const float* x, const void* delta, int delta_dtype, const float* gamma, float eps, float* x_out, void* q8,
