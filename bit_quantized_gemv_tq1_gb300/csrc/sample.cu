@@ -699,10 +699,11 @@ __device__ __noinline__ void pass() {
 }
 
 // The middle of [lo, hi], and what the farthest from it are off, with room for
-// the rounding of both and of a difference from it; without bounds 0 and infinity.
+// the rounding of both and of a difference from it (halves of subnormal values, too,
+// of which two steps are lost at most); without bounds 0 and infinity.
 __device__ __forceinline__ void middle_of(float lo, float hi, float& mid, float& half) {
   mid = 0.5f * lo + 0.5f * hi;
-  half = 0.5f * hi - 0.5f * lo + 2.4e-7f * (fabsf(lo) + fabsf(hi));
+  half = 0.5f * hi - 0.5f * lo + 2.4e-7f * (fabsf(lo) + fabsf(hi)) + 1.1e-44f;
   if (!(half < INFINITY)) {
     mid = 0.0f;
     half = INFINITY;

@@ -68,3 +68,30 @@ def test_many_infinities(tq, dtype, t, v, n):
                 place, kept = even(n, u[i], **kw)
                 assert ids[i] == at[i][place], (kw, i, u[i], ids[i], at[i][place])
                 assert abs(probs[i] - 1 / kept) <= 2.0 ** -23 / kept
+
+
+def by_logit(row):
+    return sorted(range(len(row)), key=lambda i: (-row[i], i))
+
+
+@pytest.mark.parametrize("v", [700, 5000, 70001])
+def test_subnormal_logits(tq, v):
+    """Logits of a few steps of 2^-149: halves of odd ones are rounded, and all weigh 1."""
+    x = torch.zeros(5, v)
+    steps = {0: {11: 5, 30: 4, 77: 4, 600: 3}, 1: {11: -5, 30: 4, 77: 1, 600: 3}}
+    for i in steps:
+        for at, n in steps[i].items():
+            x[i, at] = n * 2.0 ** -149
+    g = torch.Generator().manual_seed(v)
+    x[2] = torch.randint(0, 7, (v,), generator=g) * 2.0 ** -149
+    x[3] = torch.randint(-9, 0, (v,), generator=g) * 2.0 ** -149
+    x[4] = 3 * 2.0 ** -149
+    order = [by_logit(row) for row in x.tolist()]
+    dev = x.cuda()
+    for kw in (dict(top_k=2), dict(top_k=3), dict(top_k=40), dict(top_k=600), dict(), dict(top_p=0.5), dict(min_p=0.5)):
+        for u in (0.0, 0.37, 1 - 2.0 ** -24):
+            ids, probs = choose(tq, dev, [u] * 5, **kw)
+            for i in range(5):
+                place, kept = even(v, u, **kw)
+                assert ids[i] == order[i][place], (kw, i, u, order[i].index(ids[i]) if ids[i] >= 0 else -1, place)
+                assert abs(probs[i] - 1 / kept) <= 2.0 ** -23 / kept
