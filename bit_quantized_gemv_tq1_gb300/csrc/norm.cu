@@ -112,7 +112,13 @@ __device__ __forceinline__ uint32_t round8(float v, float d) {
 // The same of four values, packed: v / d is within 2e-5 of v * (1 / d) (two
 // roundings of numbers up to 127), so the nearest integer is the quantiser's
 // but where that lies within 3e-5 of a half; there (one value in 8000) the
-// quotient is formed.  The integer is read off the last bits of 1.5 2^23 + v/d.
+// quotient is formed, and where values are not finite.  The integer is read off
+// the last bits of 1.5 2^23 + v/d.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 __device__ __forceinline__ uint32_t round8x4(const float4& v, float d, float inv) {
   constexpr float kMagic = 12582912.0f;
   const float t[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
@@ -122,9 +128,9 @@ __device__ __forceinline__ uint32_t round8x4(const float4& v, float d, float inv
   for (int i = 0; i < 4; ++i) {
     const float m = __fadd_rn(t[i], kMagic);
     q[i] = __float_as_uint(m);
-    off = fmaxf(off, fabsf(t[i] - __fsub_rn(m, kMagic)));
+    off = max_or_nan(off, fabsf(t[i] - __fsub_rn(m, kMagic)));
   }
-  if (off > 0.49997f || !(d > 1e-36f)) {  // 1 / d of smaller ones is not finite
+  if (!(off <= 0.49997f) || !(d > 1e-36f)) {  // 1 / d of smaller ones is not finite
     q[0] = round8(v.x, d);
     q[1] = round8(v.y, d);
     q[2] = round8(v.z, d);

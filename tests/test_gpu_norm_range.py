@@ -77,3 +77,23 @@ def test_rows_between_leave_the_others_alone(tq):
     same = torch.ones(1300, dtype=torch.bool, device="cuda")
     same[some] = same[some + 1] = False
     assert torch.equal(ya[same], yb[same]) and torch.equal(qa[same], qb[same])
+
+
+@pytest.mark.parametrize("k", [256, 6144, 40960])
+def test_blocks_of_values_that_are_not_finite(tq, k):
+    """Finite rows whose y overflows or meets a gamma that is not finite, and rows that are not finite: q8 equals the quantiser's blocks of y."""
+    inf, nan = float("inf"), float("nan")
+    g = gen(k)
+    x, gamma = 5 * torch.randn(8, k, device="cuda", generator=g), 1 + 0.2 * torch.randn(k, device="cuda", generator=g)
+    x[0, 3], x[1, 40], x[2, 70], x[2, 71], x[3, 100] = nan, inf, -inf, nan, -inf
+    x[4, 32:64] = nan
+    x[5, 7] = 3e38
+    for values in (gamma, gamma * 3.4e38, gamma * -1e37, torch.where(torch.arange(k, device="cuda") % 37 == 5, inf, gamma),
+                   torch.where(torch.arange(k, device="cuda") % 64 == 9, nan, gamma), torch.full_like(gamma, nan), torch.full_like(gamma, -inf)):
+        q8, ref = (torch.zeros(8, k // 32, 36, dtype=torch.uint8, device="cuda") for _ in range(2))
+        y = torch.empty(8, k, device="cuda")
+        tq.tq1_rms_norm(x, values, 1e-6, q8=q8, y=y)
+        tq.q8_1_quantize_acts(y, ref, 8, k)
+        assert torch.equal(q8[..., 4:], ref[..., 4:])
+        scales, want = (b[..., :4].contiguous().view(torch.float16) for b in (q8, ref))
+        assert torch.equal(scales.isnan(), want.isnan()) and torch.equal(scales.nan_to_num(), want.nan_to_num())
