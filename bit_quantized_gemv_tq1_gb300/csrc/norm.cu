@@ -14,8 +14,8 @@
 // took 2 to 4% more of many rows without a delta.)
 //
 // A few rows wait for their loads, then for the row's sum: a row of 6144 takes
-// 3.2 us in a sequence of calls, 48 rows of 5120 with an fp32 delta 3.5.  Many
-// are bound by memory: 4096 rows of 5120 with a bf16 delta in 41.9 us, 5.6 TB/s.
+// 2.7 us in a sequence of calls, 48 rows of 5120 with an fp32 delta 3.2.  Many
+// are bound by memory: 4096 rows of 5120 with a bf16 delta in 41.4 us, 5.6 TB/s.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -38,7 +38,7 @@ constexpr uint32_t delta_size() {
 
 constexpr int kSlots = 2;                  // rows on their way, or being read
 constexpr int64_t kRowsSmem = 200 * 1024;
-constexpr int kRowsMinK = 2048;
+constexpr int kRowsMinK = 6144;
 
 // Eight values; x' = x + delta of a group.
 struct Eight {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int on
 // one is worked on.  A row's slot is free as soon as its values are in
 // registers, which the barrier of the sum says, so a row takes one barrier.
 template <typename TD, int NV>
-__global__ void __launch_bounds__(1024) rms_norm_rows_kernel(const NormArgs a, int64_t t, unsigned* status) {
+__global__ void __launch_bounds__(NV == 2 ? 512 : 544, NV == 2 ? 2 : 1) rms_norm_rows_kernel(const NormArgs a, int64_t t, unsigned* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kSlots];
   __shared__ float s_part[2][32];
@@ -445,24 +445,28 @@ template <typename TD>
 int launch_delta(const NormArgs& a, int64_t t, unsigned* status, cudaStream_t s) {
   const int sms = std::max(1, device_info().num_sms);
   const int groups = a.k >> 3;
-  // Rows copied ahead, where a row with its delta is 12 KB and more and there
-  // are several to a CTA.  4096 rows of 5120 with a 16-bit delta 47.6 -> 41.9 us
-  // (8192 of 2048 the same, of 1024 19.8 -> 25.2); with an fp32 delta no
-  // faster (49.8, 49.7), without one slower (26.4 -> 28.5): not there.
+  auto threads_of = [&](int nv) { return ((groups + nv - 1) / nv + 31) / 32 * 32; };
+  auto resident = [&](int nv) { return static_cast<int64_t>(sms) * ((nv == 1 ? 2048 : nv == 2 ? 1344 : 1024) / threads_of(nv)); };
+  // Rows copied ahead, where a row with its delta is 36 KB and more and there are
+  // several to a CTA, unless only one such CTA fits an SM where the other kernel has
+  // two rows.  With a 16-bit delta, not so and so: 4096 rows of 2048 18.2 and 20.1 us,
+  // of 4096 34.0 and 34.6; 2432 of 6144 32.7 and 32.5; 6000 of 8192 100 and 91; 4096 of
+  // 10240 82 and 99, of 11264 121 and 110.  With an fp32 delta no faster (49.8,
+  // 49.7), without one slower (26.4 and 28.5): not there.
   if constexpr (delta_size<TD>() == 2) {
-    if (t >= 8 * sms && a.k >= kRowsMinK && kSlots * static_cast<int64_t>(a.k) * 6 <= kRowsSmem) {
+    const int64_t smem = kSlots * static_cast<int64_t>(a.k) * 6;
+    if (t >= 8 * sms && a.k >= kRowsMinK && smem <= kRowsSmem && (2 * (smem + 1024) <= 228 * 1024 || resident(2) < 2 * sms)) {
       if (groups <= 2 * 512) return launch_rows<TD, 2>(a, t, ((groups + 1) / 2 + 31) / 32 * 32, status, s);
       return launch_rows<TD, 4>(a, t, ((groups + 3) / 4 + 31) / 32 * 32, status, s);
     }
   }
   // Groups of a thread: the fewest with which all rows are resident at once (a
-  // thread has 32, 44 or 62 registers), but two where one makes CTAs of 800 threads and more.
-  // One, two and four groups: 48 rows of 2080 2.6, 3.0 and 4.0 us, 517 of them 3.8, 3.7
-  // and 4.9, 1000 rows of 1024 3.1, 3.6 and 4.5; 48 rows of 8192 4.9, 4.3 and 5.1, 400 of them
-  // 10.0, 9.6 and 7.1.  Beyond that two (3000 rows of 5120 34.9, 33.1 and 35.0), unless
-  // four take two waves where two take more than three (1000 rows of 8192 18.4, 17.8 and 15.3).
-  auto threads_of = [&](int nv) { return ((groups + nv - 1) / nv + 31) / 32 * 32; };
-  auto resident = [&](int nv) { return static_cast<int64_t>(sms) * ((nv == 1 ? 2048 : nv == 2 ? 1344 : 1024) / threads_of(nv)); };
+  // thread has 32, 48 or 64 registers), but two where one makes CTAs of 800 threads and more.
+  // One, two and four groups, with an fp32 delta: 48 rows of 2080 2.3, 2.8 and 3.7 us, 517 of them
+  // 4.6, 5.0 and 6.1, 1000 rows of 1024 4.2, 4.6 and 5.8; 48 rows of 8192 4.9, 4.8 and 5.8, 400 of
+  // them 10.6, 10.7 and 10.6.  Beyond that two (3000 rows of 5120 33.5, 33.9 and 38.2, 4096 of them
+  // without a delta 31.6, 26.8 and 26.6), unless four take two waves where two take more than
+  // three (1000 rows of 8192 21.4, 20.9 and 23.2, without a delta 16.0, 14.9 and 13.5).
   int nv = 2;
   if (groups <= 768 && t <= resident(1)) nv = 1;
   else if (t > resident(2) && (t <= resident(4) || (t > 3 * resident(2) && t <= 2 * resident(4)))) nv = 4;

@@ -97,3 +97,19 @@ def test_blocks_of_values_that_are_not_finite(tq, k):
         assert torch.equal(q8[..., 4:], ref[..., 4:])
         scales, want = (b[..., :4].contiguous().view(torch.float16) for b in (q8, ref))
         assert torch.equal(scales.isnan(), want.isnan()) and torch.equal(scales.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("t,k,delta", [(1220, 6144, "bf16"), (1218, 8192, "f16"), (1216, 11264, "bf16")])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 3e38])
+def test_far_rows_among_rows_copied_ahead(tq, t, k, delta, eps):
+    g = gen(k)
+    x, d = rows_of_all_sizes(g, t, k, delta)
+    near = torch.arange(t, device="cuda") % 4 != 1
+    x[near], d[near] = even(g, t, k)[near], even(g, t, k).to(d.dtype)[near]
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    y, q8 = check(tq, x, d, None, eps, in_place=False)
+    z, p8 = check(tq, x, d, None, eps, in_place=True)
+    assert torch.equal(y, z) and torch.equal(q8, p8)
+    only = torch.empty_like(y)  # x' is not kept: it is formed again
+    tq.tq1_rms_norm(x, None, eps, y=only, delta=d)
+    assert torch.equal(only, y)
