@@ -22,9 +22,12 @@
 // rows) that every CTA finds from the ids in shared memory; a last one adds up.
 //
 // One token waits for the chain of selection, weights and h (8 of 128 experts of
-// 768 x 2048 in 10.7 us); large experts and batches are bound by the instructions of
-// expanding and multiplying (the pipe of integer products is 56 to 69% busy): 7
-// tokens of two of 8 experts of 2816 x 4096 43 us, 32 tokens of 8 of 128 89 us.
+// 768 x 2048 in 10.2 us).  Large experts and batches expand and multiply, but fill no
+// pipe: issue slots are 48 to 60% used, that of integer products 41 to 55%; the
+// rest are waits for staged weights, turns that end unevenly, and selection and sum in
+// kernels of their own.  7 tokens of two of 8 experts of 2816 x 4096 42 us, 32 tokens of
+// 8 of 128 89 us.  From some 16 pairs an expert on a pair costs the same however many
+// there are (512 tokens of 8 of 128 0.82 ms, 47 TOP/s): there are no tensor cores here.
 //
 // Units are (row, 256-block): a lane expands one block and multiplies it.  Four
 // neighbouring lanes take the same block of four rows, so that their readings of
@@ -597,8 +600,8 @@ __host__ __device__ __forceinline__ UpTaskLayout up_task_layout(int nb, int bloc
 // products are formed.
 struct TaskInfo {
   int first, pairs, range;
-  uint32_t low[1];
-  const uint8_t* src[2];
+  const uint8_t* src[2];  // first product: its rows of gate and up
+  uint32_t at;            // second product: where its rows begin in shared memory
 };
 
 // A task's rows come in stages of 16 gate and 16 up rows, long rows in stages of
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 3) moe_down_tasks_kernel(const MoeLa
     to.pairs = x.pairs;
     to.range = task - chunk * ranges;
     const uint8_t* src = a.down + (static_cast<int64_t>(x.expert) * a.k + to.range * rows) * rowbytes;
-    to.low[0] = slot * slab + low4(src);
+    to.at = slot * slab + low4(src);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // behind the plain stores and reads of two tasks before
     request(smem + slot * slab, src, min(rows, a.k - to.range * rows) * rowbytes, &bars[slot], l2_evict_first_policy());
   };
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 3) moe_down_tasks_kernel(const MoeLa
     if (more) prepare(task + gridDim.x, slot ^ 1);
     const int n = min(rows, a.k - x.range * rows);
     const bool ok = mbar_wait(&bars[slot], slot_phase(turn >> 1));
-    if (ok) rows_dots<FMT>(x.low[0], 0, 0, nbf, n, l.recs, x.pairs, l.part, n * pitch_of(nbf));
+    if (ok) rows_dots<FMT>(x.at, 0, 0, nbf, n, l.recs, x.pairs, l.part, n * pitch_of(nbf));
     if (__syncthreads_or(!ok)) {
       if (tid == 0) {
         raise_status(status, kStatusTimeout);

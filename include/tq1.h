@@ -648,7 +648,10 @@ size_t tq1_moe_workspace_size(int64_t n_experts, int64_t k, int64_t f, int64_t t
  * 10240 with f up to 65536 (longer rows where they fit the kernels' shared memory,
  * else TQ1_ERR_UNSUPPORTED: the larger k, f, n_experts and t * top_k, and TQ2_0, need
  * more); n_experts <= 1024; top_k <= 32 and <= n_experts; t * top_k <= 4096.
- * Deterministic.
+ * Made for decoding and small batches: an expert's rows are expanded once for up to
+ * six (TQ2_0: four) of its pairs and multiplied without tensor cores, so a prompt's
+ * chunk costs time in proportion to its pairs (about 50 T operations a second) and has
+ * to be cut into calls of 4096 pairs.  Deterministic.
  * No passage: a convention of this library.
  */
 int tq1_moe(const void* gate, const void* up, const void* down, int64_t n_experts, const void* q8, const float* logits,
@@ -678,8 +681,11 @@ int tq2_moe(const void* gate, const void* up, const void* down, int64_t n_expert
  * probability 0); where there are +inf, they alone are.  Logits must not change
  * under the call: a row that finds no token because they did gets id -1 and
  * probability 0 and sets TQ1_ERR_BAD_ID.
- * Weights are held as integers in units of 2^-44 and added exactly: the same
- * tokens whatever the batch.  v <= 2^19, t <= 2^20.  No workspace.
+ * Weights are formed to 2^-33 of themselves (T up to 2^100), held as integers in units
+ * of 2^-44 (the largest is 1) and added exactly: the same tokens whatever the batch.
+ * So probs is within 2^-32 + v 2^-45 of itself plus 2^-45, beside its rounding to
+ * fp32: that of a token e^-20 as likely as the first has some 16 bits, and a token less
+ * than 2^-45 as likely is not taken.  v <= 2^19, t <= 2^20.  No workspace.
  * No passage: a convention of this library.
  */
 int tq1_sample(const void* logits, int dtype, int64_t ld, int64_t t, int64_t v, const float* temperature, const int32_t* top_k,
