@@ -451,8 +451,8 @@ int launch_delta(const NormArgs& a, int64_t t, unsigned* status, cudaStream_t s)
   // several to a CTA, unless only one such CTA fits an SM where the other kernel has
   // two rows.  With a 16-bit delta, not so and so: 4096 rows of 2048 18.2 and 20.1 us,
   // of 4096 34.0 and 34.6; 2432 of 6144 32.7 and 32.5; 6000 of 8192 100 and 91; 4096 of
-  // 10240 82 and 99, of 11264 121 and 110.  With an fp32 delta no faster (49.8,
-  // 49.7), without one slower (26.4 and 28.5): not there.
+  // 10240 82 and 99, of 11264 121 and 110.  With an fp32 delta slower (4096 rows of
+  // 6144 52 and 60, of 12288 119 and 132), and without one (of 5120 26.4 and 28.5): not there.
   if constexpr (delta_size<TD>() == 2) {
     const int64_t smem = kSlots * static_cast<int64_t>(a.k) * 6;
     if (t >= 8 * sms && a.k >= kRowsMinK && smem <= kRowsSmem && (2 * (smem + 1024) <= 228 * 1024 || resident(2) < 2 * sms)) {
