@@ -204,8 +204,8 @@ __device__ __forceinline__ float inverse_root(float mean) {
 // 2^-50 sqrt(k), then lie in 2^-49 .. 2^60.  Down: values lie below 2^53, their
 // squares' sum below 2^126; those that lose bits are below 2^-126 in y.
 __device__ __forceinline__ float factor_of(float mean) {
-  if (mean >= 7.888609052210118e-31f && mean < INFINITY) return 1.0f;
-  return mean < 1.0f ? 1.2676506002282294e30f : 2.6469779601696886e-23f;  // 2^100, 2^-75
+  if (mean < 7.888609052210118e-31f) return 1.2676506002282294e30f;   // 2^-100: 2^100
+  return mean == INFINITY ? 2.6469779601696886e-23f : 1.0f;            // 2^-75; NaN stays
 }
 __device__ __forceinline__ Eight times(const Eight& v, float by) {
   return {make_float4(v.a.x * by, v.a.y * by, v.a.z * by, v.a.w * by), make_float4(v.b.x * by, v.b.y * by, v.b.z * by, v.b.w * by)};
